@@ -100,6 +100,12 @@ typedef enum { SS_F32 = 0, SS_BF16 = 1 } ss_sketch_dtype;
  * <= 0 or not finite, e.g. an all-zero state with rho = 0): that head's map
  * rows are written as zeros. */
 #define SS_DEVICE_SINGULAR_MAP 4
+/* Set by ss_prefill when a sequence's seq_start pair is not 0 <= first <= end
+ * <= rows: that sequence's state and output rows are left as they were. */
+#define SS_DEVICE_BAD_ROWS 8
+/* Set by ss_cache_write and ss_cache_read when a slot is >= the cache's slots:
+ * that sequence is left out of the call. */
+#define SS_DEVICE_BAD_SLOT 16
 
 /* Which coefficient map the non-flush read c = C q~ uses (project page,
  * "Per step · Non-flush: Coefficient vector & readout"). */
@@ -178,6 +184,48 @@ typedef struct {
     const float* beta;       /* device [B][H]; may be NULL for Mamba-2 */
     float* out;              /* device [B][H][dv] */
 } ss_step_io;
+
+/* Token rows of ss_prefill: a packed, ragged batch.  Sequence b's tokens are
+ * rows seq_start[b] .. seq_start[b+1]-1 of every tensor below; token row i of
+ * a tensor starts `<name>_stride` elements after row i-1 (0 = dense rows: q, k
+ * qk_heads * dk, v and out heads * dv, gate heads or KDA heads * dk, beta
+ * heads), so the tensors may be column ranges of a fused projection.  Within
+ * a row, heads and channels are dense. */
+typedef struct {
+    const uint16_t* q;       /* device bf16 [rows][qk_heads][dk] */
+    const uint16_t* k;       /* device bf16 [rows][qk_heads][dk] */
+    const uint16_t* v;       /* device bf16 [rows][heads][dv] */
+    const float* gate;       /* device [rows][heads] (Mamba-2 dt, GDN a) or [rows][heads][dk] (KDA a) */
+    const float* beta;       /* device [rows][heads]; may be NULL for Mamba-2 */
+    void* out;               /* device [rows][heads][dv], float or bf16 (out_dtype); overlaps no input */
+    int64_t q_stride, k_stride, v_stride, gate_stride, beta_stride, out_stride;
+                             /* elements; q, k, v, out multiples of 8, KDA's gate of 4; at least a dense row */
+    int64_t rows;            /* token rows of the tensors, 0 .. 2^31 - 1 (0: the six pointers are not read) */
+    int64_t max_tokens;      /* at least the longest sequence's tokens, or 0 = rows; picks the form that
+                              * runs (see ss_prefill), never what is computed */
+    const int32_t* seq_start;/* device int32[batch+1], 4-byte aligned */
+    const int32_t* fresh;    /* device int32[batch], 4-byte aligned, or NULL; nonzero: the sequence starts
+                              * from a zero state, and bufs->state is only written for it */
+    int32_t qk_heads;        /* heads of q and k: a divisor of the plan's heads, 0 = heads; state head h
+                              * reads q and k of head h / (heads / qk_heads) */
+    int32_t out_dtype;       /* SS_F32 or SS_BF16 */
+} ss_prefill_io;
+
+/* A cache of quantised states (the caller owns the memory).  Slot s holds one
+ * sequence's state of the layer in 8 or 4 bits: groups of 32 consecutive
+ * values along dv share a bf16 scale = bf16(fp32(max|x| / m)), m = 127 or 7;
+ * a code is the whole number nearest to the exact x / scale (ties to even,
+ * clamped to -m .. m; 0 where the scale is 0), in two's complement; the value
+ * held is code * scale.  A group that holds an infinity or a NaN reads back as NaN.
+ *   codes   8 bits: int8 [slots][H][dk][dv]
+ *           4 bits: uint8 [slots][H][dk][dv/2], the even column in the low half of a byte
+ *   scales  bf16 [slots][H][dk][dv/32] */
+typedef struct {
+    void* codes;             /* device, 16-byte aligned */
+    uint16_t* scales;        /* device, 16-byte aligned */
+    int32_t slots;           /* >= 1 */
+    int32_t bits;            /* 8 or 4 */
+} ss_cache;
 
 /* Operation codes for ss_traffic_bytes. */
 typedef enum {
@@ -290,6 +338,40 @@ ss_status ss_replay_step(ss_plan* plan, const ss_buffers* bufs, const ss_step_io
  * (SS_ERR_CUDA) is returned.  The fills are read on the device only. */
 ss_status ss_step_mixed(ss_plan* plan, const ss_buffers* bufs, const ss_step_io* io,
                         const int32_t* fill_in, int32_t* fill_out, ss_stream stream);
+
+/* Runs many tokens of every sequence through the exact recurrence: prompts
+ * (prefill), the next part of a prompt, or the few tokens of a draft to be
+ * verified.  For each token of sequence b in order, and each head,
+ *     S <- M S + b k v^T,   out = S^T q          (M, b as above)
+ * on bufs->state, which ends as the state behind the sequence's last token.
+ * A sequence of no tokens keeps its state (a fresh one becomes zero); output
+ * rows of no sequence are left as they were.  Sequences whose rows overlap
+ * each other race for the output rows they share; nothing else does.
+ * Legal at phase 0 (nothing buffered); needs bufs->state (and A for Mamba-2).
+ * Marks the sketch stale: ss_prime comes before the next non-flush step.  In
+ * a batch driven by ss_step_mixed, sequences that have tokens buffered take
+ * no rows in the call; their buffered tokens and fill counts stay valid.
+ * State, products and sums are fp32; out is rounded once.  Two forms of the
+ * same recurrence exist: token by token with the state in registers, and
+ * chunks of 64 tokens on the tensor cores. */
+ss_status ss_prefill(ss_plan* plan, const ss_buffers* bufs, const ss_prefill_io* io, ss_stream stream);
+
+/* Bytes of a cache's two buffers for this plan. */
+ss_status ss_cache_sizes(const ss_plan* plan, int32_t bits, int32_t slots, size_t* codes, size_t* scales);
+
+/* Quantises the state of sequence b into slot slots[b] (device int32[batch],
+ * 4-byte aligned), or leaves the sequence out where slots[b] < 0.  Where
+ * several sequences name one slot the last of them is kept.  Legal at phase 0:
+ * buffered tokens are not part of the state (under ss_step_mixed the caller
+ * leaves sequences with buffered tokens out).  Needs bufs->state. */
+ss_status ss_cache_write(ss_plan* plan, const ss_buffers* bufs, const ss_cache* cache, const int32_t* slots,
+                         ss_stream stream);
+
+/* Sets the state of sequence b to what slot slots[b] holds, or leaves it as
+ * it was where slots[b] < 0; several sequences may read one slot (a shared
+ * prefix).  Legal at phase 0; marks the sketch stale. */
+ss_status ss_cache_read(ss_plan* plan, const ss_buffers* bufs, const ss_cache* cache, const int32_t* slots,
+                        ss_stream stream);
 
 /* Traffic of one call for the whole batch (see ss_traffic).  tau = phase
  * before the call for SS_OP_DECODE / SS_OP_REPLAY / SS_OP_FLUSH_NO_TOKEN. */

@@ -19,6 +19,8 @@ SS_OK, SS_ERR_INVALID_ARG, SS_ERR_ALIGNMENT, SS_ERR_UNSUPPORTED, SS_ERR_SCHEDULE
 SS_DEVICE_TIMEOUT = 1
 SS_DEVICE_BAD_FILL = 2
 SS_DEVICE_SINGULAR_MAP = 4
+SS_DEVICE_BAD_ROWS = 8
+SS_DEVICE_BAD_SLOT = 16
 SS_COEF_FIXED, SS_COEF_STATE, SS_COEF_LRD = 0, 1, 2
 SS_MAMBA2, SS_GDN, SS_KDA = 0, 1, 2
 SS_F32, SS_BF16 = 0, 1
@@ -49,6 +51,19 @@ class ss_buffers(ctypes.Structure):
 
 class ss_step_io(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "gate", "beta", "out")]
+
+
+class ss_prefill_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "gate", "beta", "out")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "gate_stride", "beta_stride",
+                                              "out_stride", "rows", "max_tokens")] + \
+               [("seq_start", ctypes.c_void_p), ("fresh", ctypes.c_void_p),
+                ("qk_heads", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class ss_cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("slots", ctypes.c_int32), ("bits", ctypes.c_int32)]
 
 
 class ss_traffic(ctypes.Structure):
@@ -85,6 +100,11 @@ def lib():
             "ss_exact_step": ([P, ctypes.POINTER(ss_buffers), ctypes.POINTER(ss_step_io), P], S),
             "ss_replay_step": ([P, ctypes.POINTER(ss_buffers), ctypes.POINTER(ss_step_io), P], S),
             "ss_step_mixed": ([P, ctypes.POINTER(ss_buffers), ctypes.POINTER(ss_step_io), P, P, P], S),
+            "ss_prefill": ([P, ctypes.POINTER(ss_buffers), ctypes.POINTER(ss_prefill_io), P], S),
+            "ss_cache_sizes": ([P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
+                                ctypes.POINTER(ctypes.c_size_t)], S),
+            "ss_cache_write": ([P, ctypes.POINTER(ss_buffers), ctypes.POINTER(ss_cache), P, P], S),
+            "ss_cache_read": ([P, ctypes.POINTER(ss_buffers), ctypes.POINTER(ss_cache), P, P], S),
             "ss_traffic_bytes": ([P, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ss_traffic)], S),
             "ss_launch_count": ([], ctypes.c_uint64),
             "ss_debug_stall_next_copy": ([P, ctypes.c_int32], S),
@@ -160,6 +180,74 @@ def make_step_io(q, k, v, gate, beta, out):
     return ss_step_io(_ptr(q, "q", d["bf16"]), _ptr(k, "k", d["bf16"]), _ptr(v, "v", d["bf16"]),
                       _ptr(gate, "gate", d["f32"]), _ptr(beta, "beta", d["f32"]),
                       _ptr(out, "out", d["f32"]))
+
+
+def _rows(t, what, dtypes, rows, *tail):
+    """Pointer and row stride (elements) of a [rows, *tail] tensor whose rows are dense."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    if tuple(t.shape) != (rows, *tail):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, *tail)}")
+    width = 1
+    for size, stride in reversed(list(zip(t.shape[1:], t.stride()[1:]))):
+        if size != 1 and stride != width:
+            raise ValueError(f"{what}: heads and channels of a row must be dense")
+        width *= size
+    if rows > 1 and t.stride(0) < width:
+        raise ValueError(f"{what}: rows must not overlap")
+    return t.data_ptr(), (t.stride(0) if rows > 1 else 0)
+
+
+def _index(t, what, n, device):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise TypeError(f"{what}: expected an int32 tensor")
+    if tuple(t.shape) != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous entries, got shape {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def make_prefill_io(plan, q, k, v, gate, beta, out, seq_start, fresh=None, max_tokens=None):
+    """Arguments of ss_prefill from [rows, heads, channels] tensors (see
+    include/sketchssm.h); rows may be strided, all tensors on one device."""
+    import torch
+    d = _dt()
+    for name, t in (("q", q), ("k", k), ("v", v), ("gate", gate), ("beta", beta), ("out", out)):
+        if t is not None and isinstance(t, torch.Tensor) and t.device != q.device:
+            raise ValueError(f"{name}: on {t.device}, q on {q.device}")
+    if q.dim() != 3:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, qk_heads, {plan.dk}]")
+    n, H = q.shape[0], plan.heads
+    qh = q.shape[1]
+    if qh < 1 or H % qh:
+        raise ValueError(f"q: {qh} heads do not divide the plan's {H}")
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out: dtype {out.dtype}, expected float32 or bfloat16")
+    kda = plan.family == SS_KDA
+    pq, sq = _rows(q, "q", d["bf16"], n, qh, plan.dk)
+    pk, sk = _rows(k, "k", d["bf16"], n, qh, plan.dk)
+    pv, sv = _rows(v, "v", d["bf16"], n, H, plan.dv)
+    pg, sg = _rows(gate, "gate", d["f32"], n, H, *((plan.dk,) if kda else ()))
+    pb, sb = (None, 0) if plan.family == SS_MAMBA2 else _rows(beta, "beta", d["f32"], n, H)
+    po, so = _rows(out, "out", (out.dtype,), n, H, plan.dv)
+    return ss_prefill_io(pq, pk, pv, pg, pb, po, sq, sk, sv, sg, sb, so, n,
+                         n if max_tokens is None else int(max_tokens),
+                         _index(seq_start, "seq_start", plan.batch + 1, q.device),
+                         None if fresh is None else _index(fresh, "fresh", plan.batch, q.device),
+                         qh, SS_BF16 if out.dtype == torch.bfloat16 else SS_F32)
+
+
+def make_cache(codes, scales, slots, bits):
+    import torch
+    return ss_cache(_ptr(codes, "codes", (torch.uint8, torch.int8)), _ptr(scales, "scales", (torch.bfloat16,)),
+                    slots, bits)
 
 
 def _stream(stream):
@@ -247,6 +335,28 @@ def ss_step_mixed(plan, bufs, io, fill_in, fill_out, stream=None):
     fi = fill_in if isinstance(fill_in, int) else fill_in.data_ptr()
     fo = fill_out if isinstance(fill_out, int) else fill_out.data_ptr()
     _check(lib().ss_step_mixed(plan.handle, ctypes.byref(bufs), ctypes.byref(io), fi, fo, _stream(stream)))
+
+
+def ss_prefill(plan, bufs, io, stream=None):
+    _check(lib().ss_prefill(plan.handle, ctypes.byref(bufs), ctypes.byref(io), _stream(stream)))
+
+
+def ss_cache_sizes(plan, bits, slots):
+    """Bytes of a cache's codes and scales for this plan."""
+    codes, scales = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().ss_cache_sizes(plan.handle, int(bits), int(slots), ctypes.byref(codes), ctypes.byref(scales)))
+    return codes.value, scales.value
+
+
+def ss_cache_write(plan, bufs, cache, slots, stream=None):
+    """slots: device int32 tensor of `batch` entries (or a raw pointer)."""
+    s = slots if isinstance(slots, int) else slots.data_ptr()
+    _check(lib().ss_cache_write(plan.handle, ctypes.byref(bufs), ctypes.byref(cache), s, _stream(stream)))
+
+
+def ss_cache_read(plan, bufs, cache, slots, stream=None):
+    s = slots if isinstance(slots, int) else slots.data_ptr()
+    _check(lib().ss_cache_read(plan.handle, ctypes.byref(bufs), ctypes.byref(cache), s, _stream(stream)))
 
 
 def ss_traffic_bytes(plan, op, tau=0):

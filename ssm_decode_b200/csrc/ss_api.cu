@@ -181,6 +181,56 @@ ss_status dense_copies(ss_plan* pl, const ss::FlushParams& p, cudaStream_t st) {
     return launch_via(pl, "dense copy", [&] { return ss::launch_dense_copy(pl->cfg.dk, pl->cfg.dv, p, st); });
 }
 
+// Index and scalar-per-head arrays: 4-byte aligned.
+ss_status check_index(const void* ptr, const char* what) {
+    if (ptr == nullptr) return fail(SS_ERR_INVALID_ARG, "%s is NULL", what);
+    if ((reinterpret_cast<uintptr_t>(ptr) & 3u) != 0) return fail(SS_ERR_ALIGNMENT, "%s is not 4-byte aligned", what);
+    return SS_OK;
+}
+
+// A token-row stride: 0 = dense rows of `width` elements.
+ss_status row_stride(int64_t given, int64_t width, int64_t multiple, const char* what, long long* out) {
+    if (given == 0) given = width;
+    if (given < width) return fail(SS_ERR_INVALID_ARG, "%s %lld is below a row's %lld elements", what,
+                                   (long long)given, (long long)width);
+    // row * stride stays far inside 64 bits for every row below 2^31
+    if (given > (int64_t(1) << 30)) return fail(SS_ERR_UNSUPPORTED, "%s %lld is above 2^30", what, (long long)given);
+    if (given % multiple != 0)
+        return fail(SS_ERR_ALIGNMENT, "%s %lld is not a multiple of %lld", what, (long long)given, (long long)multiple);
+    *out = given;
+    return SS_OK;
+}
+
+ss_status check_cache_shape(int32_t bits, int32_t slots) {
+    if (bits != 8 && bits != 4) return fail(SS_ERR_UNSUPPORTED, "cache bits %d: 8 and 4 are supported", bits);
+    if (slots < 1) return fail(SS_ERR_INVALID_ARG, "cache slots %d < 1", slots);
+    return SS_OK;
+}
+
+ss_status cache_params(const ss_plan* pl, const ss_buffers* b, const ss_cache* cache, const int32_t* slots,
+                       const char* call, ss::CacheParams* p) {
+    if (pl == nullptr || b == nullptr || cache == nullptr)
+        return fail(SS_ERR_INVALID_ARG, "plan, bufs or cache is NULL");
+    if (pl->phase != 0)
+        return fail(SS_ERR_SCHEDULE, "%s needs phase 0 (phase is %d): flush first", call, pl->phase);
+    REQUIRE_PTR(b->state, "bufs->state");
+    CHECK(check_status(b));
+    CHECK(check_cache_shape(cache->bits, cache->slots));
+    REQUIRE_PTR(cache->codes, "cache->codes");
+    REQUIRE_PTR(cache->scales, "cache->scales");
+    CHECK(check_index(slots, "slots"));
+    std::memset(p, 0, sizeof *p);
+    p->state = b->state;
+    p->codes = cache->codes;
+    p->scales = cache->scales;
+    p->slot = slots;
+    p->status = b->status;
+    p->n = (long long)pl->cfg.heads * pl->cfg.dk * pl->cfg.dv;
+    p->B = pl->cfg.batch;
+    p->slots = cache->slots;
+    return SS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -508,6 +558,90 @@ ss_status ss_step_mixed(ss_plan* pl, const ss_buffers* b, const ss_step_io* io, 
     if (e == cudaSuccess) e = cudaStreamWaitEvent(st, pl->join, 0);
     if (s != SS_OK) return s;
     if (e != cudaSuccess) return fail(SS_ERR_CUDA, "mixed step: join: %s", cudaGetErrorString(e));
+    return ok();
+}
+
+ss_status ss_prefill(ss_plan* pl, const ss_buffers* b, const ss_prefill_io* io, ss_stream stream) {
+    if (pl == nullptr || b == nullptr || io == nullptr)
+        return fail(SS_ERR_INVALID_ARG, "plan, bufs or io is NULL");
+    if (pl->phase != 0)
+        return fail(SS_ERR_SCHEDULE, "ss_prefill needs phase 0 (phase is %d): flush first", pl->phase);
+    const ss_config& c = pl->cfg;
+    const bool m2 = c.family == SS_MAMBA2, kda = c.family == SS_KDA;
+    REQUIRE_PTR(b->state, "bufs->state");
+    if (m2) REQUIRE_PTR(b->A, "bufs->A");
+    CHECK(check_status(b));
+    if (io->rows < 0 || io->rows > INT32_MAX)
+        return fail(SS_ERR_INVALID_ARG, "rows %lld outside 0..2^31-1", (long long)io->rows);
+    if (io->max_tokens < 0) return fail(SS_ERR_INVALID_ARG, "max_tokens %lld < 0", (long long)io->max_tokens);
+    if (io->out_dtype != SS_F32 && io->out_dtype != SS_BF16)
+        return fail(SS_ERR_INVALID_ARG, "unknown out_dtype %d", io->out_dtype);
+    const int qh = io->qk_heads == 0 ? c.heads : io->qk_heads;
+    if (qh < 1 || c.heads % qh != 0)
+        return fail(SS_ERR_INVALID_ARG, "qk_heads %d does not divide heads %d", io->qk_heads, c.heads);
+    CHECK(check_index(io->seq_start, "io->seq_start"));
+    if (io->fresh != nullptr) CHECK(check_index(io->fresh, "io->fresh"));
+    ss::PrefillParams p;
+    std::memset(&p, 0, sizeof p);
+    const int64_t gw = kda ? int64_t(c.heads) * c.dk : c.heads;
+    CHECK(row_stride(io->q_stride, int64_t(qh) * c.dk, 8, "q_stride", &p.qs));
+    CHECK(row_stride(io->k_stride, int64_t(qh) * c.dk, 8, "k_stride", &p.ks));
+    CHECK(row_stride(io->v_stride, int64_t(c.heads) * c.dv, 8, "v_stride", &p.vs));
+    CHECK(row_stride(io->gate_stride, gw, kda ? 4 : 1, "gate_stride", &p.gs));
+    if (!m2) CHECK(row_stride(io->beta_stride, c.heads, 1, "beta_stride", &p.bs));
+    CHECK(row_stride(io->out_stride, int64_t(c.heads) * c.dv, 8, "out_stride", &p.os));
+    if (io->rows > 0) {
+        REQUIRE_PTR(io->q, "io->q");
+        REQUIRE_PTR(io->k, "io->k");
+        REQUIRE_PTR(io->v, "io->v");
+        if (kda) REQUIRE_PTR(io->gate, "io->gate");
+        else CHECK(check_index(io->gate, "io->gate"));
+        if (!m2) CHECK(check_index(io->beta, "io->beta"));
+        REQUIRE_PTR(io->out, "io->out");
+    }
+    p.state = b->state;
+    p.A = b->A;
+    p.q = io->q; p.k = io->k; p.v = io->v; p.gate = io->gate; p.beta = io->beta; p.out = io->out;
+    p.seq_start = io->seq_start;
+    p.fresh = io->fresh;
+    p.status = b->status;
+    p.rows = int(io->rows);
+    p.B = c.batch; p.H = c.heads; p.group = c.heads / qh;
+    p.out_bf16 = io->out_dtype == SS_BF16;
+    CHECK(launch_via(pl, "prefill", [&] {
+        return ss::launch_prefill_tokens(c.family, c.dk, c.dv, p, reinterpret_cast<cudaStream_t>(stream));
+    }));
+    pl->sketch_valid = 0;
+    return ok();
+}
+
+ss_status ss_cache_sizes(const ss_plan* pl, int32_t bits, int32_t slots, size_t* codes, size_t* scales) {
+    if (pl == nullptr || codes == nullptr || scales == nullptr)
+        return fail(SS_ERR_INVALID_ARG, "plan, codes or scales is NULL");
+    CHECK(check_cache_shape(bits, slots));
+    const size_t n = size_t(slots) * pl->cfg.heads * pl->cfg.dk * pl->cfg.dv;
+    *codes = n * bits / 8;
+    *scales = n / 32 * 2;
+    return ok();
+}
+
+ss_status ss_cache_write(ss_plan* pl, const ss_buffers* b, const ss_cache* cache, const int32_t* slots,
+                         ss_stream stream) {
+    ss::CacheParams p;
+    CHECK(cache_params(pl, b, cache, slots, "ss_cache_write", &p));
+    return launch_via(pl, "cache write", [&] {
+        return ss::launch_cache_write(cache->bits, p, reinterpret_cast<cudaStream_t>(stream));
+    });
+}
+
+ss_status ss_cache_read(ss_plan* pl, const ss_buffers* b, const ss_cache* cache, const int32_t* slots,
+                        ss_stream stream) {
+    ss::CacheParams p;
+    CHECK(cache_params(pl, b, cache, slots, "ss_cache_read", &p));
+    CHECK(launch_via(pl, "cache read", [&] {
+        return ss::launch_cache_read(cache->bits, p, reinterpret_cast<cudaStream_t>(stream));
+    }));
+    pl->sketch_valid = 0;
     return ok();
 }
 

@@ -6,6 +6,7 @@ is the one include/sketchssm.h documents.
 """
 from __future__ import annotations
 
+import contextlib
 import weakref
 
 import numpy as np
@@ -138,8 +139,94 @@ class DecodeLayer:
         fill_out receives (fill_in + 1) mod W."""
         B.ss_step_mixed(self.plan, self.bufs(), self.io(tok, out), fill_in, fill_out, stream)
 
+    def prefill(self, q, k, v, gate, beta, seq_start, max_tokens=None, fresh=None, out=None,
+                out_dtype=None, stream=None):
+        """Runs a packed, ragged batch of token rows through the exact
+        recurrence, from each sequence's state (zero where fresh[b] != 0) to
+        the state behind its last token: prompts, parts of prompts, drafts.
+
+        q, k [rows][qk_heads][dk] and v [rows][heads][dv] bf16, gate fp32
+        [rows][heads] (KDA [rows][heads][dk]), beta fp32 [rows][heads] (None
+        for Mamba-2); sequence b has rows seq_start[b] .. seq_start[b+1]-1
+        (device int32 [batch + 1]).  Rows may be strided, and qk_heads may
+        divide heads (shared keys).  max_tokens (a host int, at least the
+        longest sequence) lets the library pick the faster form; None takes
+        the number of rows.  Returns out [rows][heads][dv], allocated in
+        `out_dtype` (bf16 unless given) when not passed; rows of no sequence
+        are left as they were (zero in an allocated one).  Needs phase 0;
+        prime() comes before the next sketched step."""
+        import torch
+        with self._on_device(stream) as st:
+            if out is None:
+                out = torch.zeros((q.shape[0], self.heads, self.dv), device=q.device,
+                                  dtype=out_dtype or torch.bfloat16)
+            elif out_dtype not in (None, out.dtype):
+                raise TypeError(f"out: dtype {out.dtype}, out_dtype {out_dtype}")
+            if q.device != self.state.device:
+                raise ValueError(f"q: on {q.device}, the layer on {self.state.device}")
+            B.ss_prefill(self.plan, self.bufs(False),
+                         B.make_prefill_io(self.plan, q, k, v, gate, beta, out, seq_start, fresh, max_tokens), st)
+        return out
+
+    def save(self, cache, slots, stream=None):
+        """Quantises the state of sequence b into cache slot slots[b] (device
+        int32 [batch]; negative: left out).  Of several sequences that name
+        one slot the last is kept.  Needs phase 0."""
+        with self._on_device(stream) as st:
+            B.ss_cache_write(self.plan, self.bufs(False), cache.arg(self), self._slot_index(slots), st)
+
+    def restore(self, cache, slots, stream=None):
+        """Sets the state of sequence b to what cache slot slots[b] holds
+        (negative: left as it is; a slot may be read by several).  Needs
+        phase 0; prime() comes before the next sketched step."""
+        with self._on_device(stream) as st:
+            B.ss_cache_read(self.plan, self.bufs(False), cache.arg(self), self._slot_index(slots), st)
+
+    def _slot_index(self, slots):
+        return B._index(slots, "slots", self.batch, self.state.device)
+
+    @contextlib.contextmanager
+    def _on_device(self, stream):
+        """The layer's device as the current one, and the stream a call runs
+        on there: `stream`, or the device's current stream.  An allocation
+        inside belongs to that stream."""
+        import torch
+        with torch.cuda.device(self.state.device):
+            if stream is None:
+                yield torch.cuda.current_stream()
+                return
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            with torch.cuda.stream(stream):
+                yield stream
+
     def replay_step(self, tok, out=None, stream=None):
         if self.phase == self.window - 1:
             self.flush(tok, with_sketch=False, out=out, stream=stream)
         else:
             B.ss_replay_step(self.plan, self.bufs(False), self.io(tok, out), stream)
+
+
+class StateCache:
+    """Quantised states of one layer's sequences in `slots` slots, 8 or 4 bits
+    a value with a bf16 scale per 32 (see ss_cache in include/sketchssm.h):
+    prefixes kept for later sequences, or sequences swapped out.  Written and
+    read by DecodeLayer.save and .restore of any layer of the same heads and
+    dk x dv on the same device."""
+
+    def __init__(self, layer, slots, bits=8):
+        import torch
+        codes, scales = B.ss_cache_sizes(layer.plan, bits, slots)
+        self.slots, self.bits = int(slots), int(bits)
+        self.shape = (layer.heads, layer.dk, layer.dv)
+        device = layer.state.device
+        self.codes = torch.zeros((slots, layer.heads, layer.dk, layer.dv * bits // 8), dtype=torch.uint8, device=device)
+        self.scales = torch.zeros((slots, layer.heads, layer.dk, layer.dv // 32), dtype=torch.bfloat16, device=device)
+        assert self.codes.numel() == codes and self.scales.numel() * 2 == scales
+        self._arg = B.make_cache(self.codes, self.scales, self.slots, self.bits)
+
+    def arg(self, layer):
+        if (layer.heads, layer.dk, layer.dv) != self.shape or layer.state.device != self.codes.device:
+            raise ValueError(f"cache of {self.shape} on {self.codes.device}, layer of "
+                             f"{(layer.heads, layer.dk, layer.dv)} on {layer.state.device}")
+        return self._arg
