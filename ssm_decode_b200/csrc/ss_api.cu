@@ -39,6 +39,8 @@ namespace {
 thread_local std::string g_err;
 std::atomic<uint64_t> g_launches{0};
 constexpr int kSmemLimit = 227 * 1024;
+// ss_prefill runs the chunked form from this longest sequence on.
+constexpr int64_t kChunkTokens = 17;
 
 ss_status fail(ss_status s, const char* fmt, ...) {
     char buf[512];
@@ -608,7 +610,11 @@ ss_status ss_prefill(ss_plan* pl, const ss_buffers* b, const ss_prefill_io* io, 
     p.rows = int(io->rows);
     p.B = c.batch; p.H = c.heads; p.group = c.heads / qh;
     p.out_bf16 = io->out_dtype == SS_BF16;
+    const int64_t longest = io->max_tokens == 0 || io->max_tokens > io->rows ? io->rows : io->max_tokens;
+    const bool chunks = !kda && longest >= kChunkTokens;
     CHECK(launch_via(pl, "prefill", [&] {
+        if (chunks)
+            return ss::launch_prefill_chunks(c.family, c.dk, c.dv, p, reinterpret_cast<cudaStream_t>(stream));
         return ss::launch_prefill_tokens(c.family, c.dk, c.dv, p, reinterpret_cast<cudaStream_t>(stream));
     }));
     pl->sketch_valid = 0;

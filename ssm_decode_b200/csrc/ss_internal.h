@@ -142,6 +142,8 @@ cudaError_t launch_replay(int family, int dk, int dv, const StepParams& p,
 
 // Many tokens per sequence, token by token with the state in registers.
 cudaError_t launch_prefill_tokens(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream);
+// The same in chunks of 64 tokens on the tensor cores (Mamba-2, GDN).
+cudaError_t launch_prefill_chunks(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream);
 // States into / out of quantised slots.
 cudaError_t launch_cache_write(int bits, const CacheParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(int bits, const CacheParams& p, cudaStream_t stream);

@@ -76,6 +76,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
         : "memory");
 }
 
+// The bf16 form with an MN-major B (rows are K indices holding N elements;
+// SW128 column blocks of 64 elements: leading offset = bytes between blocks,
+// stride offset = bytes between groups of 8 rows): bit 16 set.
+__host__ __device__ constexpr uint32_t idesc_bf16_bmn(int M, int N) { return idesc_bf16(M, N) | (1u << 16); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc], bf16: A is K-major in TMEM, lane = row
+// of A, two K elements a column (the even one in the low half).  One thread issues.
+__device__ __forceinline__ void mma_ts_bf16(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
 // The mbarrier receives one arrival once every MMA this thread issued before
 // has completed (their results are then in TMEM and their smem reads done).
 __device__ __forceinline__ void commit(uint64_t* bar) {
