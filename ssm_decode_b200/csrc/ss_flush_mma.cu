@@ -437,11 +437,6 @@ cudaError_t flush_mma_t(const FlushParams& p, int rmax, cudaStream_t stream) {
 
 }  // namespace
 
-// The driver's tensor-map encoder, fetched once through the runtime.
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiled tensor_map_encoder() {
     static EncodeTiled fn = nullptr;
     static std::once_flag once;

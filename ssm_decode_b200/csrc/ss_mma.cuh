@@ -50,6 +50,12 @@ __device__ __forceinline__ int tile_off(int row, int col) {
     return (col >> 5) * (K * 128) + row * 128 + ((((cc >> 2) ^ (row & 7)) << 4) | ((cc & 3) << 2));
 }
 
+// The driver's tensor-map encoder, fetched once through the runtime (null if there is none).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled tensor_map_encoder();
+
 // Tensor map of the state viewed as (B*H*dk) rows of dv floats, boxes of
 // dk rows x 32 floats, 128-byte swizzle of 16-byte chunks, or of 32-byte
 // chunks with atom32 (host; cached per buffer and swizzle).

@@ -29,16 +29,22 @@
 // fp32; out is rounded once.
 //
 // Work split: one CTA per (sequence, head), one per SM (all of TMEM).
-//   8 worker warps   hold S in registers, two threads a state column, half of
-//                    the dk rows each; they make the A operands and the output;
-//   4 staging warps  run a chunk ahead: bring q, k, v (cp.async into the
-//                    tensor cores' swizzle, zeros behind the last token), the
-//                    Gram products G, then solve X (I + A) = [P; I] from the
-//                    last column back, one row of [P T; T] a thread;
-//   1 issuing warp   one lane issues the state's MMAs.
-// Roles are paced by mbarriers only.  Every wait is bounded: when one runs out
-// the kernel sets SS_DEVICE_TIMEOUT, waits (bounded) for its MMAs in flight,
-// releases its tensor memory and returns.
+//   8 worker warps    hold S in registers, two threads a state column, half of
+//                     the dk rows each; they make the A operands and write out;
+//   4 staging warps   run ahead: from the Gram products G they solve
+//                     X (I + A) = [P; I] from the last column back, one row of
+//                     [P T; T] a thread;
+//   4 service warps   one lane each: the state's MMAs; the TMA loads of q, k, v
+//                     (three chunks deep); the Gram MMAs, a chunk ahead of the
+//                     staging warps (that warp also zeroes the rows behind a
+//                     sequence's last token, whatever memory holds there).
+// The output of a chunk is stored while the next chunk's first product runs.
+// Registers move from the service warps to the workers (168 + 168 + 136 + 40
+// a thread of the four warpgroups = the 4 x 128 of the launch).  Roles are
+// paced by mbarriers only.  Every wait is bounded: when one runs out the
+// kernel sets SS_DEVICE_TIMEOUT, waits (bounded) for its MMAs and copies in
+// flight, releases its tensor memory and returns.
+#include "ss_mma.cuh"
 #include "ss_tc.cuh"
 
 namespace ss {
@@ -48,7 +54,8 @@ constexpr int C = 64;                    // tokens a chunk
 constexpr int NP = 3;                    // bf16 parts of an fp32 operand
 constexpr int NWK = 256;                 // worker threads
 constexpr int NST = 128;                 // staging threads
-constexpr int NT = NWK + NST + 32;
+constexpr int NT = NWK + NST + 128;
+constexpr int NS = 3;                    // stages of q, k, v
 constexpr int AP = C + 4;                // row pitch of A (floats): float4 rows without bank conflicts
 
 // TMEM columns (all 512).
@@ -60,26 +67,34 @@ constexpr uint32_t T_G = 448;            // Gram products (64)
 static_assert(T_SP + 64 * NP <= T_D1 && T_UP + 32 * NP <= T_D1, "operand parts overlap D1");
 
 struct PfLayout {
-    int qk[2], tp[2], v[2], a, vec[2], bars, total;
+    int qk[NS], v[NS], tp, a, vec[NS], bars, total;
 };
 // Floats of vec: decays a, b, g, t of the chunk's tokens.
 __host__ __device__ constexpr PfLayout pf_layout(int K, int V) {
     PfLayout L{};
     int o = 0;
-    for (int s = 0; s < 2; ++s) { L.qk[s] = o; o += 2 * C * K * 2; }          // q rows, k rows: dk / 64 blocks of 128 rows
-    for (int s = 0; s < 2; ++s) { L.tp[s] = o; o += NP * 2 * C * C * 2; }     // [P T; T], a 128-row block per part
-    for (int s = 0; s < 2; ++s) { L.v[s] = o; o += C * V * 2; }
+    for (int s = 0; s < NS; ++s) { L.qk[s] = o; o += 2 * C * K * 2; }         // dk / 64 blocks of 128 rows: q, k
+    L.tp = o; o += NP * 2 * C * C * 2;                                        // [P T; T], a 128-row block per part
+    for (int s = 0; s < NS; ++s) { L.v[s] = o; o += C * V * 2; }
     L.a = o; o += C * AP * 4;
-    for (int s = 0; s < 2; ++s) { L.vec[s] = o; o += 4 * C * 4; }
-    L.bars = o; o += 128;
+    for (int s = 0; s < NS; ++s) { L.vec[s] = o; o += 4 * C * 4; }
+    L.bars = o; o += 256;
     L.total = o + 1024;
     return L;
 }
 
-// 16 bytes global -> shared, or zeros (nothing is read) where !live.
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+// Box of 64 token rows of one head: x = channel, y = head, z = row.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
 }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 __device__ __forceinline__ void st_bar() { asm volatile("bar.sync 2, 128;\n" ::: "memory"); }    // staging threads
 
 // x0, x1 cut into parts, packed two to a register (x0 in the low half).  The
@@ -90,28 +105,30 @@ __device__ __forceinline__ void cut(float x0, float x1, uint32_t (&w)[NP]) {
     for (int i = 0; i < NP; ++i) {
         const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
         w[i] = __byte_perm(b0, b1, 0x7632);
-        x0 -= __uint_as_float(b0 & 0xffff0000u);
-        x1 -= __uint_as_float(b1 & 0xffff0000u);
+        const float2 r = ffma2(make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)),
+                               dup2(-1.f), make_float2(x0, x1));
+        x0 = r.x;
+        x1 = r.y;
     }
 }
 
-// N (a multiple of 32) fp32 values of this thread's lane cut into parts and
+// N (a multiple of 16) fp32 values of this thread's lane cut into parts and
 // stored as columns of NP A operands: `base` is the first part's column for
 // the thread's first value, parts `pitch` columns apart.
 template <int N>
 __device__ __forceinline__ void put_parts(uint32_t base, uint32_t pitch, const float* x) {
 #pragma unroll
-    for (int k = 0; k < N; k += 32) {
-        uint32_t w[NP][16];
+    for (int k = 0; k < N; k += 16) {
+        uint32_t w[NP][8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
             uint32_t c[NP];
             cut(x[k + 2 * i], x[k + 2 * i + 1], c);
 #pragma unroll
             for (int p = 0; p < NP; ++p) w[p][i] = c[p];
         }
 #pragma unroll
-        for (int p = 0; p < NP; ++p) tc::st16(base + p * pitch + k / 2, w[p]);
+        for (int p = 0; p < NP; ++p) tc::st8(base + p * pitch + k / 2, w[p]);
     }
 }
 
@@ -125,12 +142,22 @@ __device__ __forceinline__ void get(uint32_t a, uint32_t* r) {
     }
 }
 
+// Four MMAs: 64 elements of K of an A operand in TMEM and of a B operand whose
+// K steps of 16 are `step` 16-byte units apart.  acc = 0: the first overwrites D.
+__device__ __forceinline__ void mma_k64(uint32_t dst, uint32_t a, uint64_t b, uint32_t step, uint32_t id, uint32_t acc) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tc::mma_ts_bf16(dst, a + 8 * k, b + step * k, id, k > 0 ? 1 : acc);
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned phase) {
     return __all_sync(FULL, mbar_wait(bar, phase));
 }
 
 template <int FAM, int K, int V>
-__global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_constant__ PrefillParams p) {
+__global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_constant__ PrefillParams p,
+                                                               const __grid_constant__ CUtensorMap qmap,
+                                                               const __grid_constant__ CUtensorMap kmap,
+                                                               const __grid_constant__ CUtensorMap vmap) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     constexpr PfLayout L = pf_layout(K, V);
@@ -157,23 +184,29 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     const int chunks = (count + C - 1) / C;
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L.bars);
-    uint64_t* full = bars + 0;                                 // [2] q, k rows staged
-    uint64_t* ready = bars + 2;                                // [2] [P T; T], v and the decays staged
-    uint64_t* freed = bars + 4;                                // [2] the stage is no longer read (workers, last MMA)
-    uint64_t* gbar = bars + 6;                                 // Gram products done
-    uint64_t* sbar = bars + 7;                                 // S^T's parts written (workers)
-    uint64_t* rbar = bars + 8;                                 // R's parts written (workers)
-    uint64_t* ubar = bars + 9;                                 // t o U's parts written (workers)
-    uint64_t* d1bar = bars + 10;                               // D1 done
-    uint64_t* d2bar = bars + 11;                               // [P T; T] R done
-    uint64_t* xbar = bars + 12;                                // the state's update done
-    uint64_t* drain = bars + 13;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+    uint64_t* lbar = bars + 0;                                 // [3] a stage's copies have landed
+    uint64_t* full = bars + 3;                                 // [3] and its rows behind the end are zero
+    uint64_t* freed = bars + 6;                                // [3] the stage is no longer read (workers, last MMA)
+    uint64_t* gbar = bars + 9;                                 // Gram products done
+    uint64_t* gread = bars + 10;                               // and read (staging)
+    uint64_t* ready = bars + 11;                               // [P T; T] and the decays staged
+    uint64_t* sbar = bars + 12;                                // S^T's parts written (workers)
+    uint64_t* rbar = bars + 13;                                // R's parts written (workers)
+    uint64_t* ubar = bars + 14;                                // t o U's parts written (workers)
+    uint64_t* d1bar = bars + 15;                               // D1 done
+    uint64_t* d2bar = bars + 16;                               // [P T; T] R done
+    uint64_t* xbar = bars + 17;                                // the state's update done
+    uint64_t* drain = bars + 18;                               // [2] the issuing threads' last MMAs done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
     if (t == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(bars + i, 1);
-        mbar_init(freed, NA + 1);
-        mbar_init(freed + 1, NA + 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(lbar + i, 1);
+            mbar_init(full + i, 1);
+            mbar_init(freed + i, NA + 1);
+        }
         mbar_init(gbar, 1);
+        mbar_init(gread, NST);
+        mbar_init(ready, 1);
         mbar_init(sbar, NA);
         mbar_init(rbar, NA);
         mbar_init(ubar, NA);
@@ -181,6 +214,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
         mbar_init(d2bar, 1);
         mbar_init(xbar, 1);
         mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -196,6 +230,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
 
     if (warp < NWK / 32) {
         // ------------------------------------------------------------ workers
+        regs_inc<168>();
         const int d = (warp & 3) * 32 + lane, half = warp >> 2;
         constexpr int KH = K / 2;                              // state rows of a thread
         if ((warp & 3) * 32 < V) {
@@ -203,22 +238,42 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
             float* const sp = state + (long long)(half * KH) * V + d;
 #pragma unroll
             for (int i = 0; i < KH; ++i) S[i] = fresh ? 0.f : __ldcs(sp + i * V);
+            float o[32];                                       // tokens half * 32 .. + 31 of this state column
+            // o to the output rows of chunk c
+            auto store = [&](int c) {
+                const int live = min(C, count - c * C) - half * 32;
+                const long long at = (long long)(first + c * C + half * 32) * p.os + (long long)h * V + d;
+                if (p.out_bf16) {
+                    uint16_t* w = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r, w += p.os)
+                        if (r < live) *w = f2bf(o[r]);
+                } else {
+                    float* w = static_cast<float*>(p.out) + at;
+#pragma unroll
+                    for (int r = 0; r < 32; ++r, w += p.os)
+                        if (r < live) *w = o[r];
+                }
+            };
+            int s = 0;
+            unsigned sph = 0;
             for (int c = 0; c < chunks; ++c) {
-                const int s = c & 1;
-                const unsigned ph = c & 1, ph2 = (c >> 1) & 1;
-                const float* vec = reinterpret_cast<const float*>(sm + L.vec[s]);
+                const unsigned ph = c & 1;
+                const float* vec = reinterpret_cast<const float*>(sm + L.vec[0] + s * (4 * C * 4));
                 const float4* vb = reinterpret_cast<const float4*>(vec + C + half * 32);
                 const float4* vg = reinterpret_cast<const float4*>(vec + 2 * C + half * 32);
                 const float4* vt = reinterpret_cast<const float4*>(vec + 3 * C + half * 32);
-                const uint16_t* sv = reinterpret_cast<const uint16_t*>(sm + L.v[s]) + half * 32 * V + d;
+                const uint16_t* sv = reinterpret_cast<const uint16_t*>(sm + L.v[0] + s * (C * V * 2)) + half * 32 * V + d;
                 put_parts<KH>(tq + T_SP + half * (KH / 2), K / 2, S);
                 tc::wait_st();
                 tc::fence_before();
                 mbar_arrive(sbar);
+                if (c > 0) store(c - 1);
 
-                if (!warp_wait(d1bar, ph) || !warp_wait(ready + s, ph2)) { failed = true; break; }
+                if (!warp_wait(lbar + s, sph) || !warp_wait(full + s, sph) || !warp_wait(ready, ph) ||
+                    !warp_wait(d1bar, ph)) { failed = true; break; }
                 tc::fence_after();
-                float y[32], o[32];                            // tokens half * 32 .. + 31 of this state column
+                float y[32];
                 if (ERASE) {
                     get<32>(tq + T_D1 + C + half * 32, reinterpret_cast<uint32_t*>(y));
                     tc::wait_ld();
@@ -262,21 +317,12 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 }
                 get<32>(tq + T_D1 + half * 32, reinterpret_cast<uint32_t*>(y));
                 tc::wait_ld();
-                const int live = min(C, count - c * C) - half * 32;
-                const long long at = (long long)(first + c * C + half * 32) * p.os + (long long)h * V + d;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float4 g = vg[i];
                     const float ge[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 4 * i + e;
-                        const float x = fmaf(ge[e], y[r], o[r]);
-                        if (r < live) {
-                            if (p.out_bf16) static_cast<uint16_t*>(p.out)[at + r * p.os] = f2bf(x);
-                            else static_cast<float*>(p.out)[at + r * p.os] = x;
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e) o[4 * i + e] = fmaf(ge[e], y[4 * i + e], o[4 * i + e]);
                 }
                 const float whole = vec[2 * C + C - 1];
                 mbar_arrive(freed + s);
@@ -290,89 +336,63 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < 32; ++i) S[k + i] = fmaf(whole, S[k + i], y[i]);
                 }
+                if (++s == NS) { s = 0; sph ^= 1u; }
             }
-            if (!failed)
+            if (!failed) {
+                store(chunks - 1);
 #pragma unroll
                 for (int i = 0; i < KH; ++i) __stcs(sp + i * V, S[i]);
+            }
         }
     } else if (warp < (NWK + NST) / 32) {
         // ------------------------------------------------------------ staging
+        regs_inc<136>();
         const int st = t - NWK;                                // row of [Q; K] and of [P T; T]
+        const int row = st & (C - 1);                          // its token
+        const bool krow = st >= C;
         const float A = FAM == MAMBA2 ? p.A[h] : 0.f;
-        const uint16_t* gq = p.q + (long long)(h / p.group) * K;
-        const uint16_t* gk = p.k + (long long)(h / p.group) * K;
-        const uint16_t* gv = p.v + (long long)h * V;
-        auto load = [&](int c) {
-            const int s = c & 1, n = min(C, count - c * C);
-            const long long r0 = first + c * C;
-            float ga = FAM == MAMBA2 ? 0.f : 1.f, be = 0.f;
-            if (st < n) {
-                ga = p.gate[(r0 + st) * p.gs + h];
-                if (ERASE) be = p.beta[(r0 + st) * p.bs + h];
-            }
-            const uint32_t qk = smem_u32(sm + L.qk[s]), vv = smem_u32(sm + L.v[s]);
-            constexpr int KC = K / 8, VC = V / 8;              // 16-byte pieces of a row
-#pragma unroll 4
-            for (int i = st; i < C * KC; i += NST) {
-                const int r = i / KC, x = (i % KC) * 8;
-                const bool live = r < n;
-                const long long row = live ? r0 + r : r0;
-                cp_async16_or_zero(qk + tc::sw128h_off(2 * C, r, x), gq + row * p.qs + x, live);
-                cp_async16_or_zero(qk + tc::sw128h_off(2 * C, C + r, x), gk + row * p.ks + x, live);
-            }
-#pragma unroll 4
-            for (int i = st; i < C * VC; i += NST) {
-                const int r = i / VC, x = (i % VC) * 8;
-                const bool live = r < n;
-                cp_async16_or_zero(vv + (r * V + x) * 2, gv + (live ? r0 + r : r0) * p.vs + x, live);
-            }
-            cp_async_commit();
-            if (st < C) {
-                float* vec = reinterpret_cast<float*>(sm + L.vec[s]);
-                if (FAM == MAMBA2) {
-                    be = ga;
-                    ga = st < n ? expf(ga * A) : 1.f;
-                }
-                vec[st] = ga;
-                vec[C + st] = be;
+        float ga = 1.f, be = 0.f;                              // of token `row`, a chunk ahead
+        auto fetch = [&](int c) {
+            ga = FAM == MAMBA2 ? 0.f : 1.f;
+            be = 0.f;
+            if (c * C + row < count) {
+                const long long r = first + c * C + row;
+                ga = p.gate[r * p.gs + h];
+                if (ERASE) be = p.beta[r * p.bs + h];
             }
         };
-        load(0);
-        if (chunks > 1) load(1);
+        fetch(0);
+        int s = 0;
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
             const unsigned ph = c & 1;
-            if (c >= 2) {
-                if (!warp_wait(freed + s, ((c >> 1) - 1) & 1)) { failed = true; break; }
-                load(c);
+            float* vec = reinterpret_cast<float*>(sm + L.vec[0] + s * (4 * C * 4));
+            // G of this chunk: its stage was free to load, so its vec is free too
+            if (!warp_wait(gbar, ph)) { failed = true; break; }
+            tc::fence_after();
+            if (FAM == MAMBA2) {
+                be = ga;
+                ga = c * C + row < count ? expf(ga * A) : 1.f;
             }
-            if (c == 0 && chunks > 1) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
-            else cp_async_wait_all();
-            tc::fence_proxy_async();
+            if (!krow) {
+                vec[row] = ga;
+                vec[C + row] = be;
+            }
+            const float scale = krow ? be : 1.f;
+            float x[C];                                        // a row of [P; A], then of [P T; T]
+            get<C>(tq + T_G, reinterpret_cast<uint32_t*>(x));
+            tc::wait_ld();
             tc::fence_before();
+            mbar_arrive(gread);
             st_bar();
-            const uint32_t qk = smem_u32(sm + L.qk[s]);
-            if (st == 0) {
-                mbar_arrive(full + s);
-                tc::fence_after();
-                constexpr uint32_t id = tc::idesc_bf16(128, C);
-#pragma unroll
-                for (int k = 0; k < K / 16; ++k) {
-                    const uint32_t o = (k >> 2) * (2 * C * 128) + (k & 3) * 32;
-                    tc::mma_ss_bf16(tmem + T_G, tc::sdesc(qk + o, 16, 1024, tc::LAYOUT_SW128),
-                                    tc::sdesc(qk + C * 128 + o, 16, 1024, tc::LAYOUT_SW128), id, k > 0);
-                }
-                tc::commit(gbar);
-            }
-            float* vec = reinterpret_cast<float*>(sm + L.vec[s]);
+            if (c + 1 < chunks) fetch(c + 1);
             if (warp == NWK / 32) {                            // g and t: products from the front and from the back
                 const float2 a = reinterpret_cast<const float2*>(vec)[lane];
                 float f = a.x * a.y, r = f;
 #pragma unroll
                 for (int m = 1; m < 32; m *= 2) {
-                    const float x = __shfl_up_sync(FULL, f, m), y = __shfl_down_sync(FULL, r, m);
-                    if (lane >= m) f *= x;
-                    if (lane + m < 32) r *= y;
+                    const float fx = __shfl_up_sync(FULL, f, m), ry = __shfl_down_sync(FULL, r, m);
+                    if (lane >= m) f *= fx;
+                    if (lane + m < 32) r *= ry;
                 }
                 float fe = __shfl_up_sync(FULL, f, 1), re = __shfl_down_sync(FULL, r, 1);
                 if (lane == 0) fe = 1.f;
@@ -380,20 +400,17 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 reinterpret_cast<float2*>(vec + 2 * C)[lane] = make_float2(fe * a.x, f);
                 reinterpret_cast<float2*>(vec + 3 * C)[lane] = make_float2(re * a.y, re);
             }
-            if (!warp_wait(gbar, ph)) { failed = true; break; }
-            tc::fence_after();
-            float x[C];                                        // a row of [P; -A], then of [P T; T]
-            get<C>(tq + T_G, reinterpret_cast<uint32_t*>(x));
-            tc::wait_ld();
-            const int row = st & (C - 1);                      // token of this row
-            const bool krow = st >= C;
             {
-                const float scale = krow ? vec[C + row] : 1.f;
                 float dij = scale;
 #pragma unroll
-                for (int j = C - 1; j >= 0; --j) {             // D_ij from j = i down
-                    if (j < row) dij *= vec[j + 1];
-                    x[j] = j <= row ? dij * x[j] : 0.f;
+                for (int j = C - 4; j >= 0; j -= 4) {          // D_ij from j = i down
+                    const float4 a = *reinterpret_cast<const float4*>(vec + j);
+                    const float ae[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                    for (int e = 3; e >= 0; --e) {
+                        x[j + e] = j + e <= row ? dij * x[j + e] : 0.f;
+                        if (j + e <= row) dij *= ae[e];
+                    }
                 }
             }
             if (ERASE) {
@@ -427,8 +444,10 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                     }
                 }
             }
+            // the product with the previous chunk's [P T; T] is done with the buffer
+            if (c > 0 && !warp_wait(d2bar, ph ^ 1u)) { failed = true; break; }
             if (ERASE || !krow) {
-                unsigned char* tp = sm + L.tp[s] + st * 128;
+                unsigned char* tp = sm + L.tp + st * 128;
 #pragma unroll
                 for (int j = 0; j < C; j += 8) {
                     uint32_t w[4][NP];
@@ -441,68 +460,138 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 }
             }
             tc::fence_proxy_async();
-            tc::fence_before();
             st_bar();
-            if (st == 0) mbar_arrive(ready + s);
+            if (st == 0) mbar_arrive(ready);
+            if (++s == NS) s = 0;
         }
-        cp_async_wait_all();
-    } else if (lane == 0) {
-        // ------------------------------------------------------------ MMAs
-        constexpr int N1 = ERASE ? 2 * C : C;
-        constexpr uint32_t id1 = tc::idesc_bf16(128, N1), id3 = tc::idesc_bf16_bmn(128, K);
-        for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
-            const unsigned ph = c & 1, ph2 = (c >> 1) & 1;
-            const uint32_t qk = smem_u32(sm + L.qk[s]), tp = smem_u32(sm + L.tp[s]);
-            if (!mbar_wait(full + s, ph2) || !mbar_wait(sbar, ph)) { failed = true; break; }
-            tc::fence_after();
-#pragma unroll
-            for (int i = 0; i < NP; ++i)
-#pragma unroll
-                for (int k = 0; k < K / 16; ++k)
-                    tc::mma_ts_bf16(tmem + T_D1, tmem + T_SP + i * (K / 2) + k * 8,
-                                    tc::sdesc(qk + (k >> 2) * (2 * C * 128) + (k & 3) * 32, 16, 1024, tc::LAYOUT_SW128),
-                                    id1, i + k > 0);
-            tc::commit(d1bar);
-            // [P T; T] R, or Mamba-2's P R beside S^T q
-            auto products = [&](uint32_t dst) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i)
-#pragma unroll
-                    for (int j = 0; i + j < NP; ++j)
-#pragma unroll
-                        for (int k = 0; k < C / 16; ++k)
-                            tc::mma_ts_bf16(dst, tmem + T_RP + i * 32 + k * 8,
-                                            tc::sdesc(tp + j * (2 * C * C * 2) + k * 32, 16, 1024, tc::LAYOUT_SW128), id1,
-                                            i + j + k > 0);
-                tc::commit(d2bar);
-            };
-            if (ERASE) {
-                if (!mbar_wait(ready + s, ph2) || !mbar_wait(rbar, ph)) { failed = true; break; }
+    } else {
+        regs_dec<40>();
+        if (warp == NWK / 32 + 4 && lane == 0) {
+            // -------------------------------------------------------- the state's MMAs
+            constexpr int N1 = ERASE ? 2 * C : C;
+            constexpr uint32_t id1 = tc::idesc_bf16(128, N1), id3 = tc::idesc_bf16_bmn(128, K);
+            const uint64_t dtp = tc::sdesc(smem_u32(sm + L.tp), 16, 1024, tc::LAYOUT_SW128);
+            int s = 0;
+            unsigned sph = 0;
+            for (int c = 0; c < chunks; ++c) {
+                const unsigned ph = c & 1;
+                const uint32_t qk = smem_u32(sm + L.qk[0] + s * (2 * C * K * 2));
+                // operands further on: the byte distance / 16 added to the address field
+                const uint64_t dqk = tc::sdesc(qk, 16, 1024, tc::LAYOUT_SW128);
+                const uint64_t dkt = tc::sdesc(qk + C * 128, 2 * C * 128, 1024, tc::LAYOUT_SW128);
+                if (!mbar_wait(full + s, sph) || !mbar_wait(sbar, ph)) { failed = true; break; }
                 tc::fence_after();
-                products(tmem + T_X);
+                // (rolled loops: unrolled ones keep every operand address in registers the warp does not have)
+#pragma unroll 1
+                for (int i = 0; i < NP * (K / 64); ++i)
+                    mma_k64(tmem + T_D1, tmem + T_SP + 32 * i, dqk + uint32_t(i & (K / 64 - 1)) * (2 * C * 128 >> 4), 2, id1,
+                            i > 0);
+                tc::commit(d1bar);
+                // [P T; T] R, or Mamba-2's P R beside S^T q
+                auto products = [&](uint32_t dst) {
+#pragma unroll 1
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll 1
+                        for (int j = 0; i + j < NP; ++j)
+                            mma_k64(dst, tmem + T_RP + 32 * i, dtp + uint32_t(j) * (2 * C * C * 2 >> 4), 2, id1, i + j > 0);
+                    tc::commit(d2bar);
+                };
+                if (ERASE) {
+                    if (!mbar_wait(ready, ph) || !mbar_wait(rbar, ph)) { failed = true; break; }
+                    tc::fence_after();
+                    products(tmem + T_X);
+                }
+                if (!mbar_wait(ready, ph) || !mbar_wait(ubar, ph)) { failed = true; break; }
+                tc::fence_after();
+#pragma unroll 1
+                for (int i = 0; i < NP; ++i) mma_k64(tmem + T_X, tmem + T_UP + 32 * i, dkt, 2048 >> 4, id3, i > 0);
+                tc::commit(xbar);
+                if (!ERASE) products(tmem + T_D1 + C);
+                tc::commit(freed + s);
+                if (++s == NS) { s = 0; sph ^= 1u; }
             }
-            if (!mbar_wait(ready + s, ph2) || !mbar_wait(ubar, ph)) { failed = true; break; }
-            tc::fence_after();
+            // every MMA of this thread has completed before the memory is released
+            tc::commit(drain);
+            if (!mbar_wait(drain, 0)) failed = true;
+        } else if (warp == NWK / 32 + 5 && lane == 0) {
+            // -------------------------------------------------------- loads
+            const int hq = h / p.group;
+            int s = 0;
+            unsigned sph = 1;
+            for (int c = 0; c < chunks; ++c) {
+                if (c >= NS && !mbar_wait(freed + s, sph)) { failed = true; break; }
+                const uint32_t qk = smem_u32(sm + L.qk[0] + s * (2 * C * K * 2));
+                mbar_expect_tx(lbar + s, C * (2 * K + V) * 2);
 #pragma unroll
-            for (int i = 0; i < NP; ++i)
+                for (int j = 0; j < K / 64; ++j) {
+                    tma_load_3d(qk + j * (2 * C * 128), &qmap, 64 * j, hq, first + c * C, lbar + s);
+                    tma_load_3d(qk + j * (2 * C * 128) + C * 128, &kmap, 64 * j, hq, first + c * C, lbar + s);
+                }
+                tma_load_3d(smem_u32(sm + L.v[0] + s * (C * V * 2)), &vmap, 0, h, first + c * C, lbar + s);
+                if (++s == NS) { s = 0; sph ^= 1u; }
+            }
+        } else if (warp == NWK / 32 + 6) {
+            // -------------------------------------------------------- Gram products
+            constexpr uint32_t id = tc::idesc_bf16(128, C);
+            int s = 0;
+            unsigned sph = 0;
+            for (int c = 0; c < chunks; ++c) {
+                unsigned char* const qkp = sm + L.qk[0] + s * (2 * C * K * 2);
+                if (!warp_wait(lbar + s, sph)) { failed = true; break; }
+                const int n = count - c * C;
+                if (n < C) {                                   // zeros behind the last token
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    for (int i = lane; i < (C - n) * 8; i += 32)
 #pragma unroll
-                for (int k = 0; k < C / 16; ++k)
-                    tc::mma_ts_bf16(tmem + T_X, tmem + T_UP + i * 32 + k * 8,
-                                    tc::sdesc(qk + C * 128 + k * 2048, 2 * C * 128, 1024, tc::LAYOUT_SW128), id3, i + k > 0);
-            tc::commit(xbar);
-            if (!ERASE) products(tmem + T_D1 + C);
-            tc::commit(freed + s);
+                        for (int j = 0; j < 2 * (K / 64); ++j)
+                            *reinterpret_cast<uint4*>(qkp + j * (C * 128) + n * 128 + i * 16) = z;
+                    uint4* const vp = reinterpret_cast<uint4*>(sm + L.v[0] + s * (C * V * 2) + n * V * 2);
+                    for (int i = lane; i < (C - n) * V / 8; i += 32) vp[i] = z;
+                    tc::fence_proxy_async();
+                }
+                __syncwarp();
+                if (c > 0 && !warp_wait(gread, (c - 1) & 1)) { failed = true; break; }
+                if (lane == 0) {
+                    mbar_arrive(full + s);
+                    tc::fence_after();
+                    const uint32_t qk = smem_u32(qkp);
+#pragma unroll
+                    for (int k = 0; k < K / 16; ++k) {
+                        const uint32_t o = (k >> 2) * (2 * C * 128) + (k & 3) * 32;
+                        tc::mma_ss_bf16(tmem + T_G, tc::sdesc(qk + o, 16, 1024, tc::LAYOUT_SW128),
+                                        tc::sdesc(qk + C * 128 + o, 16, 1024, tc::LAYOUT_SW128), id, k > 0);
+                    }
+                    tc::commit(gbar);
+                }
+                __syncwarp();
+                if (++s == NS) { s = 0; sph ^= 1u; }
+            }
+            if (lane == 0) tc::commit(drain + 1);
+            if (!warp_wait(drain + 1, 0)) failed = true;
         }
-        // every MMA of this thread has completed before the memory is released
-        tc::commit(drain);
-        if (!mbar_wait(drain, 0)) failed = true;
     }
     if (failed && lane == 0) report_timeout(p.status);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     if (warp == 0) tc::dealloc(tmem, 512);
+}
+
+// Tensor map of [rows][heads][channels] bf16 token rows, boxes of 64 rows of
+// `box` channels of one head; rows behind the last are zero.
+cudaError_t token_map(const uint16_t* base, int channels, int heads, int rows, long long stride, int box, bool swizzle,
+                      CUtensorMap* out) {
+    const EncodeTiled enc = tensor_map_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {cuuint64_t(channels), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(channels) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t boxes[3] = {cuuint32_t(box), 1, C};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, boxes,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int FAM, int K, int V>
@@ -513,9 +602,13 @@ cudaError_t chunks_launch(const PrefillParams& p, cudaStream_t stream) {
     // more than half an SM's shared memory: one CTA an SM (each takes all of TMEM)
     constexpr int bytes = need > SMEM_SM / 2 + 4096 ? need : SMEM_SM / 2 + 4096;
     auto kern = prefill_chunks_kernel<FAM, K, V>;
-    const cudaError_t e = ensure_smem(kern, kc, bytes);
+    cudaError_t e = ensure_smem(kern, kc, bytes);
+    CUtensorMap qm, km, vm;
+    if (e == cudaSuccess) e = token_map(p.q, K, p.H / p.group, p.rows, p.qs, 64, true, &qm);
+    if (e == cudaSuccess) e = token_map(p.k, K, p.H / p.group, p.rows, p.ks, 64, true, &km);
+    if (e == cudaSuccess) e = token_map(p.v, V, p.H, p.rows, p.vs, V, false, &vm);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(unsigned(p.B) * unsigned(p.H)), dim3(NT), bytes, stream, p);
+    return launch_pdl(kern, dim3(unsigned(p.B) * unsigned(p.H)), dim3(NT), bytes, stream, p, qm, km, vm);
 }
 
 template <int FAM>

@@ -147,6 +147,12 @@ __device__ __forceinline__ void st16(uint32_t a, const uint32_t (&r)[16]) {
         : "memory");
 }
 
+__device__ __forceinline__ void st8(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // Byte offsets of element (row, col) in a buffer of column blocks of 32 fp32
 // values: block col / 32 holds `rows` rows of 128 bytes.
 //   sw128_off:  16-byte chunk c of row r at chunk c ^ (r % 8) (SW128);
