@@ -1,0 +1,679 @@
+// prefill_chunks_kernel: prompts through the Mamba-2 and GDN recurrences in
+// chunks of 64 tokens on the fifth-generation tensor cores.
+//
+// Chunked gated delta rule.  Within a chunk, with D_ij = a_{j+1} ... a_i (1 for
+// j = i), g_i = a_0 ... a_i, t_j = a_{j+1} ... a_63 and S the state before it,
+//     A_ij = b_i D_ij (k_i . k_j) for j < i,     R_i = b_i (v_i - g_i S^T k_i),
+//     U = (I + A)^-1 R,
+//     o_i = g_i S^T q_i + sum_{j<=i} D_ij (q_i . k_j) u_j,
+//     S  <- g_63 S + sum_j k_j (t_j u_j)^T.
+// Mamba-2 has no erase term: A = 0, u_i = dt_i v_i.  With P_ij = D_ij (q_i . k_j),
+// U = T R and P U = (P T) R for T = (I + A)^-1, so once S^T k is known one
+// product with the stacked [P T; T] gives the outputs' part and U together.
+// Decays are products of the given a, never ratios or exponentials of sums:
+// an a of 0 or a product that underflows needs no care.
+//
+// Everything that meets the state lives transposed, state column v = TMEM lane:
+//     D1  = S^T [Q; K]^T              128 x 128, K = dk     (A = S^T in TMEM)
+//     X   = R^T [P T; T]^T            128 x 128, K = 64     (A = R^T in TMEM)
+//     X   = (t o U)^T K               128 x dk,  K = 64     (A in TMEM, K rows MN-major)
+//     G   = [Q; K] K^T                128 x 64,  K = dk     (both from shared memory)
+// so the B operands are the token rows as they lie in memory, and A operands
+// are written by the threads that own a state column.
+//
+// fp32 arithmetic from bf16 operands.  q and k are bf16 already.  An fp32
+// operand is cut into three bf16 parts of eight bits each, x = x0 + x1 + x2
+// exactly; against an exact operand that is three products, between two cut
+// ones (R with [P T; T]) the six with i + j <= 2, whose dropped rest is below
+// 2^-21 of a product.  Accumulators, the state, the decays and the inverse are
+// fp32; out is rounded once.
+//
+// Work split: one CTA per (sequence, head), one per SM (all of TMEM).
+//   8 worker warps    hold S in registers, two threads a state column, half of
+//                     the dk rows each; they make the A operands and write out;
+//   4 staging warps   run ahead: from the Gram products G they solve
+//                     X (I + A) = [P; I] from the last column back, one row of
+//                     [P T; T] a thread;
+//   4 service warps   one lane each: the state's MMAs; the TMA loads of q, k, v
+//                     (three chunks deep); the Gram MMAs, a chunk ahead of the
+//                     staging warps (that warp also zeroes the rows behind a
+//                     sequence's last token, whatever memory holds there).
+// The output of a chunk is stored while the next chunk's first product runs.
+// Registers move from the service warps to the workers (168 + 168 + 136 + 40
+// a thread of the four warpgroups = the 4 x 128 of the launch).  Roles are
+// paced by mbarriers only.  Every wait is bounded: when one runs out the
+// kernel sets SS_DEVICE_TIMEOUT, waits (bounded) for its MMAs and copies in
+// flight, releases its tensor memory and returns.
+#include "ss_mma.cuh"
+#include "ss_tc.cuh"
+
+namespace ss {
+namespace {
+
+constexpr int C = 64;                    // tokens a chunk
+constexpr int NP = 3;                    // bf16 parts of an fp32 operand
+constexpr int NWK = 256;                 // worker threads
+constexpr int NST = 128;                 // staging threads
+constexpr int NT = NWK + NST + 128;
+constexpr int NS = 3;                    // stages of q, k, v
+constexpr int AP = C + 4;                // row pitch of A (floats): no bank conflicts in the fragments' loads
+constexpr int PP = 20;                   // and of a 16 x 16 block of P
+
+// TMEM columns (all 512).
+constexpr uint32_t T_X = 0;              // [P T; T] R: outputs' part, U; then the state's update (128)
+constexpr uint32_t T_SP = 128;           // S^T in parts (dk / 2 columns each); then R and t o U in parts (32 each)
+constexpr uint32_t T_RP = T_SP, T_UP = T_SP + 32 * NP;
+constexpr uint32_t T_D1 = 320;           // S^T q (64), S^T k (64); Mamba-2: the outputs' part in place of S^T k
+constexpr uint32_t T_G = 448;            // Gram products (64)
+static_assert(T_SP + 64 * NP <= T_D1 && T_UP + 32 * NP <= T_D1, "operand parts overlap D1");
+
+struct PfLayout {
+    int qk[NS], v[NS], tp, a, p, vec[NS], bars, total;
+};
+// Floats of vec: decays a, b, g, t of the chunk's tokens.
+__host__ __device__ constexpr PfLayout pf_layout(int K, int V) {
+    PfLayout L{};
+    int o = 0;
+    for (int s = 0; s < NS; ++s) { L.qk[s] = o; o += 2 * C * K * 2; }         // dk / 64 blocks of 128 rows: q, k
+    L.tp = o; o += NP * 2 * C * C * 2;                                        // [P T; T], a 128-row block per part
+    for (int s = 0; s < NS; ++s) { L.v[s] = o; o += C * V * 2; }
+    L.a = o; o += C * AP * 4;                                                 // A, and T^T above it
+    L.p = o; o += 10 * 16 * PP * 4;                                           // P's lower blocks
+    for (int s = 0; s < NS; ++s) { L.vec[s] = o; o += 4 * C * 4; }
+    L.bars = o; o += 256;
+    L.total = o + 1024;
+    return L;
+}
+
+// Box of 64 token rows of one head: x = channel, y = head, z = row.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+__device__ __forceinline__ void st_bar() { asm volatile("bar.sync 2, 128;\n" ::: "memory"); }    // staging threads
+// The same, returning whether any of them passed `x` true: they leave together.
+__device__ __forceinline__ bool st_any(bool x) {
+    unsigned r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(unsigned(x))
+        : "memory");
+    return r != 0;
+}
+
+// x0, x1 cut into parts, packed two to a register (x0 in the low half).  The
+// first parts are the leading 16 bits of what is left (8 significant ones), so
+// every difference is exact, and so is the last part.
+__device__ __forceinline__ void cut(float x0, float x1, uint32_t (&w)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const uint32_t b0 = __float_as_uint(x0), b1 = __float_as_uint(x1);
+        w[i] = __byte_perm(b0, b1, 0x7632);
+        const float2 r = ffma2(make_float2(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u)),
+                               dup2(-1.f), make_float2(x0, x1));
+        x0 = r.x;
+        x1 = r.y;
+    }
+}
+
+// N (a multiple of 16) fp32 values of this thread's lane cut into parts and
+// stored as columns of NP A operands: `base` is the first part's column for
+// the thread's first value, parts `pitch` columns apart.
+template <int N>
+__device__ __forceinline__ void put_parts(uint32_t base, uint32_t pitch, const float* x) {
+#pragma unroll
+    for (int k = 0; k < N; k += 16) {
+        uint32_t w[NP][8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t c[NP];
+            cut(x[k + 2 * i], x[k + 2 * i + 1], c);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) w[p][i] = c[p];
+        }
+#pragma unroll
+        for (int p = 0; p < NP; ++p) tc::st8(base + p * pitch + k / 2, w[p]);
+    }
+}
+
+// N columns (a multiple of 16) of this thread's lane; the caller waits.
+template <int N>
+__device__ __forceinline__ void get(uint32_t a, uint32_t* r) {
+#pragma unroll
+    for (int k = 0; k < N; k += 16) {
+        uint32_t(&x)[16] = *reinterpret_cast<uint32_t(*)[16]>(r + k);
+        tc::ld16(a + k, x);
+    }
+}
+
+// Four MMAs: 64 elements of K of an A operand in TMEM and of a B operand whose
+// K steps of 16 are `step` 16-byte units apart.  acc = 0: the first overwrites D.
+__device__ __forceinline__ void mma_k64(uint32_t dst, uint32_t a, uint64_t b, uint32_t step, uint32_t id, uint32_t acc) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tc::mma_ts_bf16(dst, a + 8 * k, b + step * k, id, k > 0 ? 1 : acc);
+}
+
+// A 16 x 16 tile by a warp: lane (g, q) = (lane / 4, lane % 4) holds columns 4q ..
+// 4q + 3 of rows g and g + 8.
+struct Tile {
+    float2 z[2][2];
+    __device__ __forceinline__ void zero() { z[0][0] = z[0][1] = z[1][0] = z[1][1] = dup2(0.f); }
+    // += A B, 16 x 16 x 16: a at row g of A (rows AP apart), b at column 4q of B (rows BP apart)
+    template <int BP>
+    __device__ __forceinline__ void product(const float* a, const float* b) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            const float4 a0 = *reinterpret_cast<const float4*>(a + k), a1 = *reinterpret_cast<const float4*>(a + 8 * AP + k);
+            const float e0[4] = {a0.x, a0.y, a0.z, a0.w}, e1[4] = {a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 r = *reinterpret_cast<const float4*>(b + (k + e) * BP);
+                const float2 lo = make_float2(r.x, r.y), hi = make_float2(r.z, r.w);
+                z[0][0] = ffma2(dup2(e0[e]), lo, z[0][0]);
+                z[0][1] = ffma2(dup2(e0[e]), hi, z[0][1]);
+                z[1][0] = ffma2(dup2(e1[e]), lo, z[1][0]);
+                z[1][1] = ffma2(dup2(e1[e]), hi, z[1][1]);
+            }
+        }
+    }
+    // to / from row g, column 4q of a tile (rows AP apart)
+    __device__ __forceinline__ void put(float* d, float sign) const {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float4*>(d + 8 * r * AP) =
+                make_float4(sign * z[r][0].x, sign * z[r][0].y, sign * z[r][1].x, sign * z[r][1].y);
+    }
+    __device__ __forceinline__ void get(const float* d) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float4 x = *reinterpret_cast<const float4*>(d + 8 * r * AP);
+            z[r][0] = make_float2(x.x, x.y);
+            z[r][1] = make_float2(x.z, x.w);
+        }
+    }
+    // transposed (rows = columns 16 kb .. of [P T; T], columns = its rows 16 rb ..)
+    // into the parts of [P T; T]
+    __device__ __forceinline__ void put_parts(unsigned char* tp, int rb, int kb, int g, int q) const {
+        tp += 2 * g + rb * 2048 + q * 512;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r7 = (4 * q + e) & 7;                    // row % 8
+            unsigned char* const lo = tp + e * 128 + (((2 * kb) ^ r7) << 4);
+            unsigned char* const hi = tp + e * 128 + (((2 * kb + 1) ^ r7) << 4);
+            uint32_t w[NP];
+            cut((&z[0][e >> 1].x)[e & 1], (&z[1][e >> 1].x)[e & 1], w);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                *reinterpret_cast<uint16_t*>(lo + i * (2 * C * C * 2)) = uint16_t(w[i]);
+                *reinterpret_cast<uint16_t*>(hi + i * (2 * C * C * 2)) = uint16_t(w[i] >> 16);
+            }
+        }
+    }
+};
+
+// A staging warp's five blocks of [P T; T]: 5 bits each, i | j << 2, 16 for T.
+__device__ constexpr unsigned jobs(unsigned a, unsigned b, unsigned c, unsigned d, unsigned e) {
+    return a | b << 5 | c << 10 | d << 15 | e << 20;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned phase) {
+    return __all_sync(FULL, mbar_wait(bar, phase));
+}
+
+template <int FAM, int K, int V>
+__global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_constant__ PrefillParams p,
+                                                               const __grid_constant__ CUtensorMap qmap,
+                                                               const __grid_constant__ CUtensorMap kmap,
+                                                               const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr PfLayout L = pf_layout(K, V);
+    constexpr int NA = 2 * V;                                  // worker threads with a state column
+    constexpr bool ERASE = FAM == GDN;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const long long u = blockIdx.x;
+    const int b = int(u / p.H), h = int(u % p.H);
+    griddep_wait();
+    griddep_launch_next();
+    const int first = p.seq_start[b], end = p.seq_start[b + 1];
+    if (first < 0 || end < first || end > p.rows) {
+        if (t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
+        return;
+    }
+    const int count = end - first;
+    const bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
+    float* const state = p.state + u * (long long)(K * V);
+    if (count == 0) {
+        if (fresh)
+            for (int i = t; i < K * V / 4; i += NT) reinterpret_cast<float4*>(state)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        return;
+    }
+    const int chunks = (count + C - 1) / C;
+
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L.bars);
+    uint64_t* lbar = bars + 0;                                 // [3] a stage's copies have landed
+    uint64_t* full = bars + 3;                                 // [3] and its rows behind the end are zero
+    uint64_t* freed = bars + 6;                                // [3] the stage is no longer read (workers, last MMA)
+    uint64_t* gbar = bars + 9;                                 // Gram products done
+    uint64_t* gread = bars + 10;                               // and read (staging)
+    uint64_t* ready = bars + 11;                               // [P T; T] and the decays staged
+    uint64_t* sbar = bars + 12;                                // [2] S^T's parts written: first, second half of a
+                                                               // worker's rows
+    uint64_t* rbar = bars + 14;                                // R's parts written (workers)
+    uint64_t* ubar = bars + 15;                                // t o U's parts written (workers)
+    uint64_t* d1bar = bars + 16;                               // D1 done
+    uint64_t* d2bar = bars + 17;                               // [P T; T] R done
+    uint64_t* xbar = bars + 18;                                // the state's update done
+    uint64_t* drain = bars + 19;                               // [2] the issuing threads' last MMAs done
+    uint64_t* vbar = bars + 21;                                // [3] the decays of a chunk are in vec
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+    if (t == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(lbar + i, 1);
+            mbar_init(full + i, 1);
+            mbar_init(freed + i, NA + 1);
+            mbar_init(vbar + i, 1);
+        }
+        mbar_init(gbar, 1);
+        mbar_init(gread, NST);
+        mbar_init(ready, 1);
+        mbar_init(sbar, NA);
+        mbar_init(sbar + 1, NA);
+        mbar_init(rbar, NA);
+        mbar_init(ubar, NA);
+        mbar_init(d1bar, 1);
+        mbar_init(d2bar, 1);
+        mbar_init(xbar, 1);
+        mbar_init(drain, 1);
+        mbar_init(drain + 1, 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::alloc(tmem_slot, 512);
+        tc::relinquish();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tq = tmem + (uint32_t(32 * (warp & 3)) << 16);    // this warp's TMEM lane quarter
+    bool failed = false;
+
+    if (warp < NWK / 32) {
+        // ------------------------------------------------------------ workers
+        regs_inc<168>();
+        const int d = (warp & 3) * 32 + lane, half = warp >> 2;
+        constexpr int KH = K / 2;                              // state rows of a thread
+    } else if (warp < (NWK + NST) / 32) {
+        // ------------------------------------------------------------ staging
+        regs_inc<136>();
+        const int st = t - NWK;                                // row of [Q; K] and of [P T; T]
+        const int row = st & (C - 1);                          // its token
+        const bool krow = st >= C;
+        const int sw = warp - NWK / 32;
+        float* const sa = reinterpret_cast<float*>(sm + L.a);
+        float* const sp = reinterpret_cast<float*>(sm + L.p);
+        // [P T; T] is zero above its diagonal blocks, which nothing else writes
+        for (int i = st; i < NP * 2 * C * C * 2 / 16; i += NST) reinterpret_cast<uint4*>(sm + L.tp)[i] = make_uint4(0, 0, 0, 0);
+        st_bar();
+        int s = 0;
+        unsigned sph = 0;
+        for (int c = 0; c < chunks; ++c) {
+            const unsigned ph = c & 1;
+            const float* vec = reinterpret_cast<const float*>(sm + L.vec[0] + s * (4 * C * 4));
+            if (st_any(!warp_wait(vbar + s, sph) || !warp_wait(gbar, ph))) { failed = true; break; }
+            tc::fence_after();
+            // P and A = D o G, 16 columns at a time from the diagonal down (D_ij
+            // is a running product along the row).  Mamba-2: P goes straight to
+            // its parts, once the product with the previous chunk's is done.
+            if (!ERASE && st_any(c > 0 && !warp_wait(d2bar, ph ^ 1u))) { failed = true; break; }
+            {
+                const int rb = row >> 4;
+                float dij = krow ? vec[C + row] : 1.f;
+#pragma unroll 1
+                for (int kb = 3; kb >= 0; --kb) {
+                    uint32_t xr[16];
+                    tc::ld16(tq + T_G + 16 * kb, xr);
+                    tc::wait_ld();
+                    if (kb > rb) continue;
+                    float x[16];
+#pragma unroll
+                    for (int j = 12; j >= 0; j -= 4) {
+                        const float4 a = *reinterpret_cast<const float4*>(vec + 16 * kb + j);
+                        const float ae[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int e = 3; e >= 0; --e) {
+                            const bool in = 16 * kb + j + e <= row;
+                            x[j + e] = in ? dij * __uint_as_float(xr[j + e]) : 0.f;
+                            if (in) dij *= ae[e];
+                        }
+                    }
+                    if (ERASE) {                               // blocks stored transposed: [column][row]
+                        float* const dst = krow ? sa + (16 * rb) * AP + 16 * kb + (row & 15)
+                                                : sp + (rb * (rb + 1) / 2 + kb) * (16 * PP) + (row & 15);
+                        const int pitch = krow ? AP : PP;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) dst[j * pitch] = x[j];
+                    } else if (!krow) {
+                        unsigned char* tp = sm + L.tp + st * 128;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8) {
+                            uint32_t w[4][NP];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) cut(x[j + 2 * e], x[j + 2 * e + 1], w[e]);
+#pragma unroll
+                            for (int i = 0; i < NP; ++i)
+                                *reinterpret_cast<uint4*>(tp + i * (2 * C * C * 2) + (((2 * kb + (j >> 3)) ^ (st & 7)) << 4)) =
+                                    make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+                        }
+                    }
+                }
+                tc::fence_before();
+                mbar_arrive(gread);
+            }
+            if (ERASE) {
+                // T = (I + A)^-1 and P T by 16 x 16 blocks, T kept transposed above A.
+                // (Loops stay rolled: the kernel's straight-line code is what its
+                // warps wait for otherwise, instruction fetches.)
+                st_bar();
+                // T_ww: lane j solves column j (forward, in registers), and T_ww^T
+                // takes the place of A_ww, which this warp alone reads.
+                {
+                    float* const blk = sa + (16 * sw) * (AP + 1);
+                    float y[16];
+                    const int j = lane & 15;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+                    for (int k = 0; k < 15; ++k)
+#pragma unroll
+                        for (int i = (k + 1) & ~3; i < 16; i += 4) {
+                            const float4 r = *reinterpret_cast<const float4*>(blk + k * AP + i);
+                            if (i > k) y[i] = fmaf(-r.x, y[k], y[i]);
+                            if (i + 1 > k) y[i + 1] = fmaf(-r.y, y[k], y[i + 1]);
+                            if (i + 2 > k) y[i + 2] = fmaf(-r.z, y[k], y[i + 2]);
+                            y[i + 3] = fmaf(-r.w, y[k], y[i + 3]);
+                        }
+                    __syncwarp();
+                    if (lane < 16)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<float4*>(blk + j * AP + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+                }
+                st_bar();
+                // Block column j = this warp, transposed, from the diagonal down:
+                //     T_ij^T = -(sum_{j<=k<i} T_kj^T A_ik^T) T_ii^T.
+                const int g = lane >> 2, q = lane & 3;
+#pragma unroll 1
+                for (int i = sw + 1; i < 4; ++i) {
+                    Tile w;
+                    w.zero();
+#pragma unroll 1
+                    for (int k = sw; k < i; ++k)
+                        w.product<AP>(sa + (16 * sw + g) * AP + 16 * k, sa + (16 * i) * AP + 16 * k + 4 * q);
+                    // by way of A_ij's place, which nothing reads any more
+                    float* const a = sa + (16 * i + g) * AP + 16 * sw;
+                    __syncwarp();
+                    w.put(a + 4 * q, -1.f);
+                    __syncwarp();
+                    w.zero();
+                    w.product<AP>(a, sa + (16 * i) * AP + 16 * i + 4 * q);
+                    w.put(sa + (16 * sw + g) * AP + 16 * i + 4 * q, 1.f);
+                    __syncwarp();
+                }
+                // the product with the previous chunk's [P T; T] is done with the buffer
+                if (st_any(c > 0 && !warp_wait(d2bar, ph ^ 1u))) { failed = true; break; }
+                // Five blocks a warp into their parts, T_ij or
+                // (P T)_ij^T = sum_{j<=k<=i} T_kj^T P_ik^T (five products a warp).
+                unsigned todo = sw == 0 ? jobs(0, 3, 16, 17, 18) : sw == 1 ? jobs(2, 1, 19, 21, 22)
+                                        : sw == 2 ? jobs(7, 6, 23, 26, 27) : jobs(11, 5, 15, 10, 31);
+#pragma unroll 1
+                for (int n = 0; n < 5; ++n, todo >>= 5) {
+                    const int i = todo & 3, j = (todo >> 2) & 3, is_t = (todo >> 4) & 1;
+                    Tile w;
+                    if (is_t) {
+                        w.get(sa + (16 * j + g) * AP + 16 * i + 4 * q);
+                    } else {
+                        w.zero();
+#pragma unroll 1
+                        for (int k = j; k <= i; ++k)
+                            w.product<PP>(sa + (16 * j + g) * AP + 16 * k, sp + (i * (i + 1) / 2 + k) * (16 * PP) + 4 * q);
+                    }
+                    w.put_parts(sm + L.tp, i + 4 * is_t, j, g, q);
+                }
+            }
+            tc::fence_proxy_async();
+            st_bar();
+            if (st == 0) mbar_arrive(ready);
+            if (++s == NS) { s = 0; sph ^= 1u; }
+        }
+    } else {
+        regs_dec<40>();
+        if (warp == NWK / 32 + 4 && lane == 0) {
+            // -------------------------------------------------------- the state's MMAs
+            constexpr int N1 = ERASE ? 2 * C : C;
+            constexpr uint32_t id1 = tc::idesc_bf16(128, N1), id3 = tc::idesc_bf16_bmn(128, K);
+            const uint64_t dtp = tc::sdesc(smem_u32(sm + L.tp), 16, 1024, tc::LAYOUT_SW128);
+            int s = 0;
+            unsigned sph = 0;
+            for (int c = 0; c < chunks; ++c) {
+                const unsigned ph = c & 1;
+                const uint32_t qk = smem_u32(sm + L.qk[0] + s * (2 * C * K * 2));
+                // operands further on: the byte distance / 16 added to the address field
+                const uint64_t dqk = tc::sdesc(qk, 16, 1024, tc::LAYOUT_SW128);
+                const uint64_t dkt = tc::sdesc(qk + C * 128, 2 * C * 128, 1024, tc::LAYOUT_SW128);
+                if (!mbar_wait(full + s, sph)) { failed = true; break; }
+                // (rolled loops: unrolled ones keep every operand address in registers the warp does not have)
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {                  // halves of the workers' rows
+                    if (!mbar_wait(sbar + i, ph)) { failed = true; break; }
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int j = 0; j < 2 * NP; ++j) {         // part, worker half
+                        const uint32_t k0 = (j & 1) * (K / 32) + i * (K / 64);
+#pragma unroll
+                        for (int e = 0; e < K / 64; ++e) {
+                            const uint32_t k = k0 + e;
+                            tc::mma_ts_bf16(tmem + T_D1, tmem + T_SP + (j >> 1) * (K / 2) + k * 8,
+                                            dqk + (k >> 2) * (2 * C * 128 >> 4) + (k & 3) * 2, id1, i + j + e > 0);
+                        }
+                    }
+                }
+                if (failed) break;
+                tc::commit(d1bar);
+                // [P T; T] R, or Mamba-2's P R beside S^T q
+                auto products = [&](uint32_t dst) {
+#pragma unroll 1
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll 1
+                        for (int j = 0; i + j < NP; ++j)
+                            mma_k64(dst, tmem + T_RP + 32 * i, dtp + uint32_t(j) * (2 * C * C * 2 >> 4), 2, id1, i + j > 0);
+                    tc::commit(d2bar);
+                };
+                if (ERASE) {
+                    if (!mbar_wait(ready, ph) || !mbar_wait(rbar, ph)) { failed = true; break; }
+                    tc::fence_after();
+                    products(tmem + T_X);
+                }
+                if (!mbar_wait(ready, ph) || !mbar_wait(ubar, ph)) { failed = true; break; }
+                tc::fence_after();
+#pragma unroll 1
+                for (int i = 0; i < NP; ++i) mma_k64(tmem + T_X, tmem + T_UP + 32 * i, dkt, 2048 >> 4, id3, i > 0);
+                tc::commit(xbar);
+                if (!ERASE) products(tmem + T_D1 + C);
+                tc::commit(freed + s);
+                if (++s == NS) { s = 0; sph ^= 1u; }
+            }
+            // every MMA of this thread has completed before the memory is released
+            tc::commit(drain);
+            if (!mbar_wait(drain, 0)) failed = true;
+        } else if (warp == NWK / 32 + 5 && lane == 0) {
+            // -------------------------------------------------------- loads
+            const int hq = h / p.group;
+            int s = 0;
+            unsigned sph = 1;
+            for (int c = 0; c < chunks; ++c) {
+                if (c >= NS && !mbar_wait(freed + s, sph)) { failed = true; break; }
+                const uint32_t qk = smem_u32(sm + L.qk[0] + s * (2 * C * K * 2));
+                mbar_expect_tx(lbar + s, C * (2 * K + V) * 2);
+#pragma unroll
+                for (int j = 0; j < K / 64; ++j) {
+                    tma_load_3d(qk + j * (2 * C * 128), &qmap, 64 * j, hq, first + c * C, lbar + s);
+                    tma_load_3d(qk + j * (2 * C * 128) + C * 128, &kmap, 64 * j, hq, first + c * C, lbar + s);
+                }
+                tma_load_3d(smem_u32(sm + L.v[0] + s * (C * V * 2)), &vmap, 0, h, first + c * C, lbar + s);
+                if (++s == NS) { s = 0; sph ^= 1u; }
+            }
+        } else if (warp == NWK / 32 + 6) {
+            // -------------------------------------------------------- Gram products
+            constexpr uint32_t id = tc::idesc_bf16(128, C);
+            int s = 0;
+            unsigned sph = 0;
+            for (int c = 0; c < chunks; ++c) {
+                unsigned char* const qkp = sm + L.qk[0] + s * (2 * C * K * 2);
+                if (!warp_wait(lbar + s, sph)) { failed = true; break; }
+                const int n = count - c * C;
+                if (n < C) {                                   // zeros behind the last token
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    for (int i = lane; i < (C - n) * 8; i += 32)
+#pragma unroll
+                        for (int j = 0; j < 2 * (K / 64); ++j)
+                            *reinterpret_cast<uint4*>(qkp + j * (C * 128) + n * 128 + i * 16) = z;
+                    uint4* const vp = reinterpret_cast<uint4*>(sm + L.v[0] + s * (C * V * 2) + n * V * 2);
+                    for (int i = lane; i < (C - n) * V / 8; i += 32) vp[i] = z;
+                    tc::fence_proxy_async();
+                }
+                __syncwarp();
+                if (c > 0 && !warp_wait(gread, (c - 1) & 1)) { failed = true; break; }
+                if (lane == 0) {
+                    mbar_arrive(full + s);
+                    tc::fence_after();
+                    const uint32_t qk = smem_u32(qkp);
+#pragma unroll
+                    for (int k = 0; k < K / 16; ++k) {
+                        const uint32_t o = (k >> 2) * (2 * C * 128) + (k & 3) * 32;
+                        tc::mma_ss_bf16(tmem + T_G, tc::sdesc(qk + o, 16, 1024, tc::LAYOUT_SW128),
+                                        tc::sdesc(qk + C * 128 + o, 16, 1024, tc::LAYOUT_SW128), id, k > 0);
+                    }
+                    tc::commit(gbar);
+                }
+                __syncwarp();
+                if (++s == NS) { s = 0; sph ^= 1u; }
+            }
+            if (lane == 0) tc::commit(drain + 1);
+            if (!warp_wait(drain + 1, 0)) failed = true;
+        } else if (warp == NWK / 32 + 7) {
+            // -------------------------------------------------------- decays: a, b, g, t of two tokens a lane
+            const float A = FAM == MAMBA2 ? p.A[h] : 0.f;
+            float ga[2], be[2];
+            auto fetch = [&](int c) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = c * C + 2 * lane + e;
+                    ga[e] = FAM == MAMBA2 ? 0.f : 1.f;         // behind the last token: a = 1, b = 0
+                    be[e] = 0.f;
+                    if (i < count) {
+                        ga[e] = p.gate[(long long)(first + i) * p.gs + h];
+                        if (ERASE) be[e] = p.beta[(long long)(first + i) * p.bs + h];
+                    }
+                }
+            };
+            fetch(0);
+            int s = 0;
+            unsigned sph = 1;
+            for (int c = 0; c < chunks; ++c) {
+                if (c >= NS && !warp_wait(freed + s, sph)) { failed = true; break; }
+                float2* vec = reinterpret_cast<float2*>(sm + L.vec[0] + s * (4 * C * 4));
+                float2 a = make_float2(ga[0], ga[1]), bt = make_float2(be[0], be[1]);
+                if (FAM == MAMBA2) {
+                    bt = a;
+                    a = make_float2(expf(a.x * A), expf(a.y * A));
+                }
+                if (c + 1 < chunks) fetch(c + 1);
+                float f = a.x * a.y, r = f;                    // products from the front and from the back
+#pragma unroll
+                for (int m = 1; m < 32; m *= 2) {
+                    const float fx = __shfl_up_sync(FULL, f, m), ry = __shfl_down_sync(FULL, r, m);
+                    if (lane >= m) f *= fx;
+                    if (lane + m < 32) r *= ry;
+                }
+                float fe = __shfl_up_sync(FULL, f, 1), re = __shfl_down_sync(FULL, r, 1);
+                if (lane == 0) fe = 1.f;
+                if (lane == 31) re = 1.f;
+                vec[lane] = a;
+                vec[C / 2 + lane] = bt;
+                vec[C + lane] = make_float2(fe * a.x, f);
+                vec[3 * C / 2 + lane] = make_float2(re * a.y, re);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(vbar + s);
+                if (++s == NS) { s = 0; sph ^= 1u; }
+            }
+        }
+    }
+    if (failed && lane == 0) report_timeout(p.status);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 0) tc::dealloc(tmem, 512);
+}
+
+// Tensor map of [rows][heads][channels] bf16 token rows, boxes of 64 rows of
+// `box` channels of one head; rows behind the last are zero.
+cudaError_t token_map(const uint16_t* base, int channels, int heads, int rows, long long stride, int box, bool swizzle,
+                      CUtensorMap* out) {
+    const EncodeTiled enc = tensor_map_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {cuuint64_t(channels), cuuint64_t(heads), cuuint64_t(rows)};
+    const cuuint64_t strides[2] = {cuuint64_t(channels) * 2, cuuint64_t(stride) * 2};
+    const cuuint32_t boxes[3] = {cuuint32_t(box), 1, C};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(base), dims, strides, boxes,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int FAM, int K, int V>
+cudaError_t chunks_launch(const PrefillParams& p, cudaStream_t stream) {
+    static KernelCache kc;
+    constexpr int need = pf_layout(K, V).total;
+    static_assert(need <= SMEM_LIMIT, "shared memory");
+    // more than half an SM's shared memory: one CTA an SM (each takes all of TMEM)
+    constexpr int bytes = need > SMEM_SM / 2 + 4096 ? need : SMEM_SM / 2 + 4096;
+    auto kern = prefill_chunks_kernel<FAM, K, V>;
+    cudaError_t e = ensure_smem(kern, kc, bytes);
+    CUtensorMap qm, km, vm;
+    if (e == cudaSuccess) e = token_map(p.q, K, p.H / p.group, p.rows, p.qs, 64, true, &qm);
+    if (e == cudaSuccess) e = token_map(p.k, K, p.H / p.group, p.rows, p.ks, 64, true, &km);
+    if (e == cudaSuccess) e = token_map(p.v, V, p.H, p.rows, p.vs, V, false, &vm);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(unsigned(p.B) * unsigned(p.H)), dim3(NT), bytes, stream, p, qm, km, vm);
+}
+
+template <int FAM>
+cudaError_t chunks_dispatch(int dk, int dv, const PrefillParams& p, cudaStream_t stream) {
+    if (dk == 128 && dv == 128) return chunks_launch<FAM, 128, 128>(p, stream);
+    if (dk == 128 && dv == 64) return chunks_launch<FAM, 128, 64>(p, stream);
+    if (dk == 64 && dv == 128) return chunks_launch<FAM, 64, 128>(p, stream);
+    if (dk == 64 && dv == 64) return chunks_launch<FAM, 64, 64>(p, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_chunks(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream) {
+    if (family == GDN) return chunks_dispatch<GDN>(dk, dv, p, stream);
+    if (family == MAMBA2) return chunks_dispatch<MAMBA2>(dk, dv, p, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace ss
