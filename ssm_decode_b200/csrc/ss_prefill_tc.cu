@@ -56,8 +56,7 @@ constexpr int NWK = 256;                 // worker threads
 constexpr int NST = 128;                 // staging threads
 constexpr int NT = NWK + NST + 128;
 constexpr int NS = 3;                    // stages of q, k, v
-constexpr int AP = C + 4;                // row pitch of A (floats): no bank conflicts in the fragments' loads
-constexpr int PP = 20;                   // and of a 16 x 16 block of P
+constexpr int AP = C + 4;                // row pitch of A (floats): float4 rows without bank conflicts
 
 // TMEM columns (all 512).
 constexpr uint32_t T_X = 0;              // [P T; T] R: outputs' part, U; then the state's update (128)
@@ -68,7 +67,7 @@ constexpr uint32_t T_G = 448;            // Gram products (64)
 static_assert(T_SP + 64 * NP <= T_D1 && T_UP + 32 * NP <= T_D1, "operand parts overlap D1");
 
 struct PfLayout {
-    int qk[NS], v[NS], tp, a, p, vec[NS], bars, total;
+    int qk[NS], v[NS], tp, a, vec[NS], bars, total;
 };
 // Floats of vec: decays a, b, g, t of the chunk's tokens.
 __host__ __device__ constexpr PfLayout pf_layout(int K, int V) {
@@ -77,8 +76,7 @@ __host__ __device__ constexpr PfLayout pf_layout(int K, int V) {
     for (int s = 0; s < NS; ++s) { L.qk[s] = o; o += 2 * C * K * 2; }         // dk / 64 blocks of 128 rows: q, k
     L.tp = o; o += NP * 2 * C * C * 2;                                        // [P T; T], a 128-row block per part
     for (int s = 0; s < NS; ++s) { L.v[s] = o; o += C * V * 2; }
-    L.a = o; o += C * AP * 4;                                                 // A, and T^T above it
-    L.p = o; o += 10 * 16 * PP * 4;                                           // P's lower blocks
+    L.a = o; o += C * AP * 4;
     for (int s = 0; s < NS; ++s) { L.vec[s] = o; o += 4 * C * 4; }
     L.bars = o; o += 256;
     L.total = o + 1024;
@@ -98,16 +96,6 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 __device__ __forceinline__ void st_bar() { asm volatile("bar.sync 2, 128;\n" ::: "memory"); }    // staging threads
-// The same, returning whether any of them passed `x` true: they leave together.
-__device__ __forceinline__ bool st_any(bool x) {
-    unsigned r;
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-        : "=r"(r)
-        : "r"(unsigned(x))
-        : "memory");
-    return r != 0;
-}
 
 // x0, x1 cut into parts, packed two to a register (x0 in the low half).  The
 // first parts are the leading 16 bits of what is left (8 significant ones), so
@@ -161,69 +149,6 @@ __device__ __forceinline__ void mma_k64(uint32_t dst, uint32_t a, uint64_t b, ui
     for (int k = 0; k < 4; ++k) tc::mma_ts_bf16(dst, a + 8 * k, b + step * k, id, k > 0 ? 1 : acc);
 }
 
-// A 16 x 16 tile by a warp: lane (g, q) = (lane / 4, lane % 4) holds columns 4q ..
-// 4q + 3 of rows g and g + 8.
-struct Tile {
-    float2 z[2][2];
-    __device__ __forceinline__ void zero() { z[0][0] = z[0][1] = z[1][0] = z[1][1] = dup2(0.f); }
-    // += A B, 16 x 16 x 16: a at row g of A (rows AP apart), b at column 4q of B (rows BP apart)
-    template <int BP>
-    __device__ __forceinline__ void product(const float* a, const float* b) {
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-            const float4 a0 = *reinterpret_cast<const float4*>(a + k), a1 = *reinterpret_cast<const float4*>(a + 8 * AP + k);
-            const float e0[4] = {a0.x, a0.y, a0.z, a0.w}, e1[4] = {a1.x, a1.y, a1.z, a1.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 r = *reinterpret_cast<const float4*>(b + (k + e) * BP);
-                const float2 lo = make_float2(r.x, r.y), hi = make_float2(r.z, r.w);
-                z[0][0] = ffma2(dup2(e0[e]), lo, z[0][0]);
-                z[0][1] = ffma2(dup2(e0[e]), hi, z[0][1]);
-                z[1][0] = ffma2(dup2(e1[e]), lo, z[1][0]);
-                z[1][1] = ffma2(dup2(e1[e]), hi, z[1][1]);
-            }
-        }
-    }
-    // to / from row g, column 4q of a tile (rows AP apart)
-    __device__ __forceinline__ void put(float* d, float sign) const {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<float4*>(d + 8 * r * AP) =
-                make_float4(sign * z[r][0].x, sign * z[r][0].y, sign * z[r][1].x, sign * z[r][1].y);
-    }
-    __device__ __forceinline__ void get(const float* d) {
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float4 x = *reinterpret_cast<const float4*>(d + 8 * r * AP);
-            z[r][0] = make_float2(x.x, x.y);
-            z[r][1] = make_float2(x.z, x.w);
-        }
-    }
-    // transposed (rows = columns 16 kb .. of [P T; T], columns = its rows 16 rb ..)
-    // into the parts of [P T; T]
-    __device__ __forceinline__ void put_parts(unsigned char* tp, int rb, int kb, int g, int q) const {
-        tp += 2 * g + rb * 2048 + q * 512;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r7 = (4 * q + e) & 7;                    // row % 8
-            unsigned char* const lo = tp + e * 128 + (((2 * kb) ^ r7) << 4);
-            unsigned char* const hi = tp + e * 128 + (((2 * kb + 1) ^ r7) << 4);
-            uint32_t w[NP];
-            cut((&z[0][e >> 1].x)[e & 1], (&z[1][e >> 1].x)[e & 1], w);
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                *reinterpret_cast<uint16_t*>(lo + i * (2 * C * C * 2)) = uint16_t(w[i]);
-                *reinterpret_cast<uint16_t*>(hi + i * (2 * C * C * 2)) = uint16_t(w[i] >> 16);
-            }
-        }
-    }
-};
-
-// A staging warp's five blocks of [P T; T]: 5 bits each, i | j << 2, 16 for T.
-__device__ constexpr unsigned jobs(unsigned a, unsigned b, unsigned c, unsigned d, unsigned e) {
-    return a | b << 5 | c << 10 | d << 15 | e << 20;
-}
-
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned phase) {
     return __all_sync(FULL, mbar_wait(bar, phase));
 }
@@ -265,28 +190,24 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     uint64_t* gbar = bars + 9;                                 // Gram products done
     uint64_t* gread = bars + 10;                               // and read (staging)
     uint64_t* ready = bars + 11;                               // [P T; T] and the decays staged
-    uint64_t* sbar = bars + 12;                                // [2] S^T's parts written: first, second half of a
-                                                               // worker's rows
-    uint64_t* rbar = bars + 14;                                // R's parts written (workers)
-    uint64_t* ubar = bars + 15;                                // t o U's parts written (workers)
-    uint64_t* d1bar = bars + 16;                               // D1 done
-    uint64_t* d2bar = bars + 17;                               // [P T; T] R done
-    uint64_t* xbar = bars + 18;                                // the state's update done
-    uint64_t* drain = bars + 19;                               // [2] the issuing threads' last MMAs done
-    uint64_t* vbar = bars + 21;                                // [3] the decays of a chunk are in vec
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+    uint64_t* sbar = bars + 12;                                // S^T's parts written (workers)
+    uint64_t* rbar = bars + 13;                                // R's parts written (workers)
+    uint64_t* ubar = bars + 14;                                // t o U's parts written (workers)
+    uint64_t* d1bar = bars + 15;                               // D1 done
+    uint64_t* d2bar = bars + 16;                               // [P T; T] R done
+    uint64_t* xbar = bars + 17;                                // the state's update done
+    uint64_t* drain = bars + 18;                               // [2] the issuing threads' last MMAs done
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
     if (t == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(lbar + i, 1);
             mbar_init(full + i, 1);
             mbar_init(freed + i, NA + 1);
-            mbar_init(vbar + i, 1);
         }
         mbar_init(gbar, 1);
         mbar_init(gread, NST);
         mbar_init(ready, 1);
         mbar_init(sbar, NA);
-        mbar_init(sbar + 1, NA);
         mbar_init(rbar, NA);
         mbar_init(ubar, NA);
         mbar_init(d1bar, 1);
@@ -343,17 +264,13 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 const float4* vg = reinterpret_cast<const float4*>(vec + 2 * C + half * 32);
                 const float4* vt = reinterpret_cast<const float4*>(vec + 3 * C + half * 32);
                 const uint16_t* sv = reinterpret_cast<const uint16_t*>(sm + L.v[0] + s * (C * V * 2)) + half * 32 * V + d;
-                // in two steps, so that the first product starts on the first
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    put_parts<KH / 2>(tq + T_SP + half * (KH / 2) + i * (KH / 4), K / 2, S + i * (KH / 2));
-                    tc::wait_st();
-                    tc::fence_before();
-                    mbar_arrive(sbar + i);
-                }
+                put_parts<KH>(tq + T_SP + half * (KH / 2), K / 2, S);
+                tc::wait_st();
+                tc::fence_before();
+                mbar_arrive(sbar);
                 if (c > 0) store(c - 1);
 
-                if (!warp_wait(lbar + s, sph) || !warp_wait(full + s, sph) || !warp_wait(vbar + s, sph) || !warp_wait(ready, ph) ||
+                if (!warp_wait(lbar + s, sph) || !warp_wait(full + s, sph) || !warp_wait(ready, ph) ||
                     !warp_wait(d1bar, ph)) { failed = true; break; }
                 tc::fence_after();
                 float y[32];
@@ -433,141 +350,119 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
         const int st = t - NWK;                                // row of [Q; K] and of [P T; T]
         const int row = st & (C - 1);                          // its token
         const bool krow = st >= C;
-        const int sw = warp - NWK / 32;
-        float* const sa = reinterpret_cast<float*>(sm + L.a);
-        float* const sp = reinterpret_cast<float*>(sm + L.p);
-        // [P T; T] is zero above its diagonal blocks, which nothing else writes
-        for (int i = st; i < NP * 2 * C * C * 2 / 16; i += NST) reinterpret_cast<uint4*>(sm + L.tp)[i] = make_uint4(0, 0, 0, 0);
-        st_bar();
+        const float A = FAM == MAMBA2 ? p.A[h] : 0.f;
+        float ga = 1.f, be = 0.f;                              // of token `row`, a chunk ahead
+        auto fetch = [&](int c) {
+            ga = FAM == MAMBA2 ? 0.f : 1.f;
+            be = 0.f;
+            if (c * C + row < count) {
+                const long long r = first + c * C + row;
+                ga = p.gate[r * p.gs + h];
+                if (ERASE) be = p.beta[r * p.bs + h];
+            }
+        };
+        fetch(0);
         int s = 0;
-        unsigned sph = 0;
         for (int c = 0; c < chunks; ++c) {
             const unsigned ph = c & 1;
-            const float* vec = reinterpret_cast<const float*>(sm + L.vec[0] + s * (4 * C * 4));
-            if (st_any(!warp_wait(vbar + s, sph) || !warp_wait(gbar, ph))) { failed = true; break; }
+            float* vec = reinterpret_cast<float*>(sm + L.vec[0] + s * (4 * C * 4));
+            // G of this chunk: its stage was free to load, so its vec is free too
+            if (!warp_wait(gbar, ph)) { failed = true; break; }
             tc::fence_after();
-            // P and A = D o G, 16 columns at a time from the diagonal down (D_ij
-            // is a running product along the row).  Mamba-2: P goes straight to
-            // its parts, once the product with the previous chunk's is done.
-            if (!ERASE && st_any(c > 0 && !warp_wait(d2bar, ph ^ 1u))) { failed = true; break; }
+            if (FAM == MAMBA2) {
+                be = ga;
+                ga = c * C + row < count ? expf(ga * A) : 1.f;
+            }
+            if (!krow) {
+                vec[row] = ga;
+                vec[C + row] = be;
+            }
+            const float scale = krow ? be : 1.f;
+            float x[C];                                        // a row of [P; A], then of [P T; T]
+            get<C>(tq + T_G, reinterpret_cast<uint32_t*>(x));
+            tc::wait_ld();
+            tc::fence_before();
+            mbar_arrive(gread);
+            st_bar();
+            if (c + 1 < chunks) fetch(c + 1);
+            if (warp == NWK / 32) {                            // g and t: products from the front and from the back
+                const float2 a = reinterpret_cast<const float2*>(vec)[lane];
+                float f = a.x * a.y, r = f;
+#pragma unroll
+                for (int m = 1; m < 32; m *= 2) {
+                    const float fx = __shfl_up_sync(FULL, f, m), ry = __shfl_down_sync(FULL, r, m);
+                    if (lane >= m) f *= fx;
+                    if (lane + m < 32) r *= ry;
+                }
+                float fe = __shfl_up_sync(FULL, f, 1), re = __shfl_down_sync(FULL, r, 1);
+                if (lane == 0) fe = 1.f;
+                if (lane == 31) re = 1.f;
+                reinterpret_cast<float2*>(vec + 2 * C)[lane] = make_float2(fe * a.x, f);
+                reinterpret_cast<float2*>(vec + 3 * C)[lane] = make_float2(re * a.y, re);
+            }
             {
-                const int rb = row >> 4;
-                float dij = krow ? vec[C + row] : 1.f;
-#pragma unroll 1
-                for (int kb = 3; kb >= 0; --kb) {
-                    uint32_t xr[16];
-                    tc::ld16(tq + T_G + 16 * kb, xr);
-                    tc::wait_ld();
-                    if (kb > rb) continue;
-                    float x[16];
+                float dij = scale;
 #pragma unroll
-                    for (int j = 12; j >= 0; j -= 4) {
-                        const float4 a = *reinterpret_cast<const float4*>(vec + 16 * kb + j);
-                        const float ae[4] = {a.x, a.y, a.z, a.w};
+                for (int j = C - 4; j >= 0; j -= 4) {          // D_ij from j = i down
+                    const float4 a = *reinterpret_cast<const float4*>(vec + j);
+                    const float ae[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                        for (int e = 3; e >= 0; --e) {
-                            const bool in = 16 * kb + j + e <= row;
-                            x[j + e] = in ? dij * __uint_as_float(xr[j + e]) : 0.f;
-                            if (in) dij *= ae[e];
-                        }
-                    }
-                    if (ERASE) {                               // blocks stored transposed: [column][row]
-                        float* const dst = krow ? sa + (16 * rb) * AP + 16 * kb + (row & 15)
-                                                : sp + (rb * (rb + 1) / 2 + kb) * (16 * PP) + (row & 15);
-                        const int pitch = krow ? AP : PP;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) dst[j * pitch] = x[j];
-                    } else if (!krow) {
-                        unsigned char* tp = sm + L.tp + st * 128;
-#pragma unroll
-                        for (int j = 0; j < 16; j += 8) {
-                            uint32_t w[4][NP];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) cut(x[j + 2 * e], x[j + 2 * e + 1], w[e]);
-#pragma unroll
-                            for (int i = 0; i < NP; ++i)
-                                *reinterpret_cast<uint4*>(tp + i * (2 * C * C * 2) + (((2 * kb + (j >> 3)) ^ (st & 7)) << 4)) =
-                                    make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
-                        }
+                    for (int e = 3; e >= 0; --e) {
+                        x[j + e] = j + e <= row ? dij * x[j + e] : 0.f;
+                        if (j + e <= row) dij *= ae[e];
                     }
                 }
-                tc::fence_before();
-                mbar_arrive(gread);
             }
             if (ERASE) {
-                // T = (I + A)^-1 and P T by 16 x 16 blocks, T kept transposed above A.
-                // (Loops stay rolled: the kernel's straight-line code is what its
-                // warps wait for otherwise, instruction fetches.)
+                if (krow) {
+                    float* sa = reinterpret_cast<float*>(sm + L.a) + row * AP;
+#pragma unroll
+                    for (int j = 0; j < C; j += 4)
+                        *reinterpret_cast<float4*>(sa + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+#pragma unroll
+                    for (int j = 0; j < C; ++j) x[j] = j == row ? 1.f : 0.f;
+                }
                 st_bar();
-                // T_ww: lane j solves column j (forward, in registers), and T_ww^T
-                // takes the place of A_ww, which this warp alone reads.
-                {
-                    float* const blk = sa + (16 * sw) * (AP + 1);
-                    float y[16];
-                    const int j = lane & 15;
+                // X (I + A) = [P; I]: x_m is final once every later one has been
+                // taken out; then x_j -= x_m A_mj for the j before it.
+                const float* sa = reinterpret_cast<const float*>(sm + L.a);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = i == j ? 1.f : 0.f;
+                for (int m = C - 1; m > 0; --m) {
+                    const float2 xm = dup2(-x[m]);
 #pragma unroll
-                    for (int k = 0; k < 15; ++k)
-#pragma unroll
-                        for (int i = (k + 1) & ~3; i < 16; i += 4) {
-                            const float4 r = *reinterpret_cast<const float4*>(blk + k * AP + i);
-                            if (i > k) y[i] = fmaf(-r.x, y[k], y[i]);
-                            if (i + 1 > k) y[i + 1] = fmaf(-r.y, y[k], y[i + 1]);
-                            if (i + 2 > k) y[i + 2] = fmaf(-r.z, y[k], y[i + 2]);
-                            y[i + 3] = fmaf(-r.w, y[k], y[i + 3]);
+                    for (int j = ((m - 1) & ~3); j >= 0; j -= 4) {
+                        const float4 a = *reinterpret_cast<const float4*>(sa + m * AP + j);
+                        if (j + 3 < m) {
+                            const float2 hi = ffma2(xm, make_float2(a.z, a.w), make_float2(x[j + 2], x[j + 3]));
+                            const float2 lo = ffma2(xm, make_float2(a.x, a.y), make_float2(x[j], x[j + 1]));
+                            x[j] = lo.x; x[j + 1] = lo.y; x[j + 2] = hi.x; x[j + 3] = hi.y;
+                        } else {
+                            if (j + 2 < m) x[j + 2] = fmaf(xm.x, a.z, x[j + 2]);
+                            if (j + 1 < m) x[j + 1] = fmaf(xm.x, a.y, x[j + 1]);
+                            x[j] = fmaf(xm.x, a.x, x[j]);
                         }
-                    __syncwarp();
-                    if (lane < 16)
-#pragma unroll
-                        for (int i = 0; i < 16; i += 4)
-                            *reinterpret_cast<float4*>(blk + j * AP + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-                }
-                st_bar();
-                // Block column j = this warp, transposed, from the diagonal down:
-                //     T_ij^T = -(sum_{j<=k<i} T_kj^T A_ik^T) T_ii^T.
-                const int g = lane >> 2, q = lane & 3;
-#pragma unroll 1
-                for (int i = sw + 1; i < 4; ++i) {
-                    Tile w;
-                    w.zero();
-#pragma unroll 1
-                    for (int k = sw; k < i; ++k)
-                        w.product<AP>(sa + (16 * sw + g) * AP + 16 * k, sa + (16 * i) * AP + 16 * k + 4 * q);
-                    float* const z = sa + (16 * sw + g) * AP + 16 * i;     // T_ij^T's place, by way of it
-                    w.put(z + 4 * q, -1.f);
-                    __syncwarp();
-                    w.zero();
-                    w.product<AP>(z, sa + (16 * i) * AP + 16 * i + 4 * q);
-                    __syncwarp();
-                    w.put(z + 4 * q, 1.f);
-                    __syncwarp();
-                }
-                // the product with the previous chunk's [P T; T] is done with the buffer
-                if (st_any(c > 0 && !warp_wait(d2bar, ph ^ 1u))) { failed = true; break; }
-                // Five blocks a warp into their parts, T_ij or
-                // (P T)_ij^T = sum_{j<=k<=i} T_kj^T P_ik^T (five products a warp).
-                unsigned todo = sw == 0 ? jobs(0, 3, 16, 17, 18) : sw == 1 ? jobs(2, 1, 19, 21, 22)
-                                        : sw == 2 ? jobs(7, 6, 23, 26, 27) : jobs(11, 5, 15, 10, 31);
-#pragma unroll 1
-                for (int n = 0; n < 5; ++n, todo >>= 5) {
-                    const int i = todo & 3, j = (todo >> 2) & 3, is_t = (todo >> 4) & 1;
-                    Tile w;
-                    if (is_t) {
-                        w.get(sa + (16 * j + g) * AP + 16 * i + 4 * q);
-                    } else {
-                        w.zero();
-#pragma unroll 1
-                        for (int k = j; k <= i; ++k)
-                            w.product<PP>(sa + (16 * j + g) * AP + 16 * k, sp + (i * (i + 1) / 2 + k) * (16 * PP) + 4 * q);
                     }
-                    w.put_parts(sm + L.tp, i + 4 * is_t, j, g, q);
+                }
+            }
+            // the product with the previous chunk's [P T; T] is done with the buffer
+            if (c > 0 && !warp_wait(d2bar, ph ^ 1u)) { failed = true; break; }
+            if (ERASE || !krow) {
+                unsigned char* tp = sm + L.tp + st * 128;
+#pragma unroll
+                for (int j = 0; j < C; j += 8) {
+                    uint32_t w[4][NP];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) cut(x[j + 2 * e], x[j + 2 * e + 1], w[e]);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        *reinterpret_cast<uint4*>(tp + q * (2 * C * C * 2) + (((j >> 3) ^ (st & 7)) << 4)) =
+                            make_uint4(w[0][q], w[1][q], w[2][q], w[3][q]);
                 }
             }
             tc::fence_proxy_async();
             st_bar();
             if (st == 0) mbar_arrive(ready);
-            if (++s == NS) { s = 0; sph ^= 1u; }
+            if (++s == NS) s = 0;
         }
     } else {
         regs_dec<40>();
@@ -584,24 +479,13 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 // operands further on: the byte distance / 16 added to the address field
                 const uint64_t dqk = tc::sdesc(qk, 16, 1024, tc::LAYOUT_SW128);
                 const uint64_t dkt = tc::sdesc(qk + C * 128, 2 * C * 128, 1024, tc::LAYOUT_SW128);
-                if (!mbar_wait(full + s, sph)) { failed = true; break; }
+                if (!mbar_wait(full + s, sph) || !mbar_wait(sbar, ph)) { failed = true; break; }
+                tc::fence_after();
                 // (rolled loops: unrolled ones keep every operand address in registers the warp does not have)
 #pragma unroll 1
-                for (int i = 0; i < 2; ++i) {                  // halves of the workers' rows
-                    if (!mbar_wait(sbar + i, ph)) { failed = true; break; }
-                    tc::fence_after();
-#pragma unroll 1
-                    for (int j = 0; j < 2 * NP; ++j) {         // part, worker half
-                        const uint32_t k0 = (j & 1) * (K / 32) + i * (K / 64);
-#pragma unroll
-                        for (int e = 0; e < K / 64; ++e) {
-                            const uint32_t k = k0 + e;
-                            tc::mma_ts_bf16(tmem + T_D1, tmem + T_SP + (j >> 1) * (K / 2) + k * 8,
-                                            dqk + (k >> 2) * (2 * C * 128 >> 4) + (k & 3) * 2, id1, i + j + e > 0);
-                        }
-                    }
-                }
-                if (failed) break;
+                for (int i = 0; i < NP * (K / 64); ++i)
+                    mma_k64(tmem + T_D1, tmem + T_SP + 32 * i, dqk + uint32_t(i & (K / 64 - 1)) * (2 * C * 128 >> 4), 2, id1,
+                            i > 0);
                 tc::commit(d1bar);
                 // [P T; T] R, or Mamba-2's P R beside S^T q
                 auto products = [&](uint32_t dst) {
@@ -684,52 +568,6 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
             }
             if (lane == 0) tc::commit(drain + 1);
             if (!warp_wait(drain + 1, 0)) failed = true;
-        } else if (warp == NWK / 32 + 7) {
-            // -------------------------------------------------------- decays: a, b, g, t of two tokens a lane
-            const float A = FAM == MAMBA2 ? p.A[h] : 0.f;
-            float ga[2], be[2];
-            auto fetch = [&](int c) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = c * C + 2 * lane + e;
-                    ga[e] = FAM == MAMBA2 ? 0.f : 1.f;         // behind the last token: a = 1, b = 0
-                    be[e] = 0.f;
-                    if (i < count) {
-                        ga[e] = p.gate[(long long)(first + i) * p.gs + h];
-                        if (ERASE) be[e] = p.beta[(long long)(first + i) * p.bs + h];
-                    }
-                }
-            };
-            fetch(0);
-            int s = 0;
-            unsigned sph = 1;
-            for (int c = 0; c < chunks; ++c) {
-                if (c >= NS && !warp_wait(freed + s, sph)) { failed = true; break; }
-                float2* vec = reinterpret_cast<float2*>(sm + L.vec[0] + s * (4 * C * 4));
-                float2 a = make_float2(ga[0], ga[1]), bt = make_float2(be[0], be[1]);
-                if (FAM == MAMBA2) {
-                    bt = a;
-                    a = make_float2(expf(a.x * A), expf(a.y * A));
-                }
-                if (c + 1 < chunks) fetch(c + 1);
-                float f = a.x * a.y, r = f;                    // products from the front and from the back
-#pragma unroll
-                for (int m = 1; m < 32; m *= 2) {
-                    const float fx = __shfl_up_sync(FULL, f, m), ry = __shfl_down_sync(FULL, r, m);
-                    if (lane >= m) f *= fx;
-                    if (lane + m < 32) r *= ry;
-                }
-                float fe = __shfl_up_sync(FULL, f, 1), re = __shfl_down_sync(FULL, r, 1);
-                if (lane == 0) fe = 1.f;
-                if (lane == 31) re = 1.f;
-                vec[lane] = a;
-                vec[C / 2 + lane] = bt;
-                vec[C + lane] = make_float2(fe * a.x, f);
-                vec[3 * C / 2 + lane] = make_float2(re * a.y, re);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(vbar + s);
-                if (++s == NS) { s = 0; sph ^= 1u; }
-            }
         }
     }
     if (failed && lane == 0) report_timeout(p.status);
