@@ -56,6 +56,7 @@ constexpr int NWK = 256;                 // worker threads
 constexpr int NST = 128;                 // staging threads
 constexpr int NT = NWK + NST + 128;
 constexpr int NS = 3;                    // stages of q, k, v
+constexpr int SORT = 256;                // up to so many sequences are taken longest first
 constexpr int AP = C + 4;                // row pitch of A (floats): float4 rows without bank conflicts
 
 // TMEM columns (all 512).
@@ -95,7 +96,18 @@ template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
-__device__ __forceinline__ void st_bar() { asm volatile("bar.sync 2, 128;\n" ::: "memory"); }    // staging threads
+// Named barrier of the staging threads, and the same returning whether any of
+// them passed `x` true: they leave together.
+__device__ __forceinline__ bool st_any(bool x) {
+    unsigned r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(unsigned(x))
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void st_bar() { asm volatile("bar.sync 2, 128;\n" ::: "memory"); }
 
 // x0, x1 cut into parts, packed two to a register (x0 in the low half).  The
 // first parts are the leading 16 bits of what is left (8 significant ones), so
@@ -164,10 +176,25 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     constexpr int NA = 2 * V;                                  // worker threads with a state column
     constexpr bool ERASE = FAM == GDN;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const long long u = blockIdx.x;
-    const int b = int(u / p.H), h = int(u % p.H);
     griddep_wait();
     griddep_launch_next();
+    const int h = int(blockIdx.x % unsigned(p.H));
+    int b = int(blockIdx.x / unsigned(p.H));
+    if (p.B > 1 && p.B <= SORT) {
+        // CTAs start in order: the b-th longest sequence, so that none of the
+        // long ones begins last
+        int* const len = reinterpret_cast<int*>(sm);
+        if (t < p.B) len[t] = p.seq_start[t + 1] - p.seq_start[t];
+        __syncthreads();
+        int rank = 0;
+        if (t < p.B)
+            for (int j = 0; j < p.B; ++j) rank += len[j] > len[t] || (len[j] == len[t] && j < t);
+        __syncthreads();
+        if (t < p.B && rank == b) len[0] = t;
+        __syncthreads();
+        b = len[0];
+        __syncthreads();
+    }
     const int first = p.seq_start[b], end = p.seq_start[b + 1];
     if (first < 0 || end < first || end > p.rows) {
         if (t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
@@ -175,7 +202,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     }
     const int count = end - first;
     const bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
-    float* const state = p.state + u * (long long)(K * V);
+    float* const state = p.state + ((long long)b * p.H + h) * (K * V);
     if (count == 0) {
         if (fresh)
             for (int i = t; i < K * V / 4; i += NT) reinterpret_cast<float4*>(state)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -367,7 +394,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
             const unsigned ph = c & 1;
             float* vec = reinterpret_cast<float*>(sm + L.vec[0] + s * (4 * C * 4));
             // G of this chunk: its stage was free to load, so its vec is free too
-            if (!warp_wait(gbar, ph)) { failed = true; break; }
+            if (st_any(!warp_wait(gbar, ph))) { failed = true; break; }
             tc::fence_after();
             if (FAM == MAMBA2) {
                 be = ga;
@@ -445,7 +472,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 }
             }
             // the product with the previous chunk's [P T; T] is done with the buffer
-            if (c > 0 && !warp_wait(d2bar, ph ^ 1u)) { failed = true; break; }
+            if (st_any(c > 0 && !warp_wait(d2bar, ph ^ 1u))) { failed = true; break; }
             if (ERASE || !krow) {
                 unsigned char* tp = sm + L.tp + st * 128;
 #pragma unroll
