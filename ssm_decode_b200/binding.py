@@ -182,66 +182,71 @@ def make_step_io(q, k, v, gate, beta, out):
                       _ptr(out, "out", d["f32"]))
 
 
-def _rows(t, what, dtypes, rows, *tail):
-    """Pointer and row stride (elements) of a [rows, *tail] tensor whose rows are dense."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch.Tensor")
+def _rows(t, what, dtypes, shape, device):
+    """Pointer and row stride (elements, 0 = dense) of a [rows, ...] tensor whose rows are dense."""
+    try:
+        if t.is_contiguous() and t.shape == shape and t.dtype in dtypes and t.device == device:
+            return t.data_ptr(), 0
+    except AttributeError:
+        raise TypeError(f"{what}: expected a torch.Tensor") from None
     if t.dtype not in dtypes:
         raise TypeError(f"{what}: dtype {t.dtype} not in {dtypes}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: must be a CUDA tensor")
-    if tuple(t.shape) != (rows, *tail):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {(rows, *tail)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {shape}")
     width = 1
     for size, stride in reversed(list(zip(t.shape[1:], t.stride()[1:]))):
         if size != 1 and stride != width:
             raise ValueError(f"{what}: heads and channels of a row must be dense")
         width *= size
-    if rows > 1 and t.stride(0) < width:
+    if t.shape[0] > 1 and t.stride(0) < width:
         raise ValueError(f"{what}: rows must not overlap")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else 0)
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else 0)
 
 
 def _index(t, what, n, device):
     import torch
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
         raise TypeError(f"{what}: expected an int32 tensor")
-    if tuple(t.shape) != (n,) or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous entries, got shape {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
     return t.data_ptr()
 
 
-def make_prefill_io(plan, q, k, v, gate, beta, out, seq_start, fresh=None, max_tokens=None):
+def make_prefill_io(plan, q, k, v, gate, beta, out, seq_start, fresh=None, max_tokens=None, device=None):
     """Arguments of ss_prefill from [rows, heads, channels] tensors (see
-    include/sketchssm.h); rows may be strided, all tensors on one device."""
+    include/sketchssm.h); rows may be strided, all tensors on one CUDA device
+    (q's unless given)."""
     import torch
-    d = _dt()
-    for name, t in (("q", q), ("k", k), ("v", v), ("gate", gate), ("beta", beta), ("out", out)):
-        if t is not None and isinstance(t, torch.Tensor) and t.device != q.device:
-            raise ValueError(f"{name}: on {t.device}, q on {q.device}")
+    f32, bf16 = (torch.float32,), (torch.bfloat16, torch.int16, torch.uint16)
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q: expected a torch.Tensor")
+    if device is None:
+        device = q.device
+    if device.type != "cuda":
+        raise ValueError("q: must be a CUDA tensor")
     if q.dim() != 3:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected [rows, qk_heads, {plan.dk}]")
-    n, H = q.shape[0], plan.heads
-    qh = q.shape[1]
+    n, qh, _ = q.shape
+    H = plan.heads
     if qh < 1 or H % qh:
         raise ValueError(f"q: {qh} heads do not divide the plan's {H}")
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"out: dtype {out.dtype}, expected float32 or bfloat16")
-    kda = plan.family == SS_KDA
-    pq, sq = _rows(q, "q", d["bf16"], n, qh, plan.dk)
-    pk, sk = _rows(k, "k", d["bf16"], n, qh, plan.dk)
-    pv, sv = _rows(v, "v", d["bf16"], n, H, plan.dv)
-    pg, sg = _rows(gate, "gate", d["f32"], n, H, *((plan.dk,) if kda else ()))
-    pb, sb = (None, 0) if plan.family == SS_MAMBA2 else _rows(beta, "beta", d["f32"], n, H)
-    po, so = _rows(out, "out", (out.dtype,), n, H, plan.dv)
+    if not isinstance(out, torch.Tensor) or out.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out: expected a float32 or bfloat16 tensor")
+    pq, sq = _rows(q, "q", bf16, (n, qh, plan.dk), device)
+    pk, sk = _rows(k, "k", bf16, (n, qh, plan.dk), device)
+    pv, sv = _rows(v, "v", bf16, (n, H, plan.dv), device)
+    pg, sg = _rows(gate, "gate", f32, (n, H, plan.dk) if plan.family == SS_KDA else (n, H), device)
+    pb, sb = (None, 0) if plan.family == SS_MAMBA2 else _rows(beta, "beta", f32, (n, H), device)
+    po, so = _rows(out, "out", (out.dtype,), (n, H, plan.dv), device)
     return ss_prefill_io(pq, pk, pv, pg, pb, po, sq, sk, sv, sg, sb, so, n,
                          n if max_tokens is None else int(max_tokens),
-                         _index(seq_start, "seq_start", plan.batch + 1, q.device),
-                         None if fresh is None else _index(fresh, "fresh", plan.batch, q.device),
-                         qh, SS_BF16 if out.dtype == torch.bfloat16 else SS_F32)
+                         _index(seq_start, "seq_start", plan.batch + 1, device),
+                         None if fresh is None else _index(fresh, "fresh", plan.batch, device),
+                         qh, SS_BF16 if out.dtype is torch.bfloat16 else SS_F32)
 
 
 def make_cache(codes, scales, slots, bits):

@@ -158,14 +158,13 @@ class DecodeLayer:
         import torch
         with self._on_device(stream) as st:
             if out is None:
-                out = torch.zeros((q.shape[0], self.heads, self.dv), device=q.device,
+                out = torch.zeros((q.shape[0], self.heads, self.dv), device=self.state.device,
                                   dtype=out_dtype or torch.bfloat16)
             elif out_dtype not in (None, out.dtype):
                 raise TypeError(f"out: dtype {out.dtype}, out_dtype {out_dtype}")
-            if q.device != self.state.device:
-                raise ValueError(f"q: on {q.device}, the layer on {self.state.device}")
-            B.ss_prefill(self.plan, self.bufs(False),
-                         B.make_prefill_io(self.plan, q, k, v, gate, beta, out, seq_start, fresh, max_tokens), st)
+            B.ss_prefill(self.plan, self._bufs[False],
+                         B.make_prefill_io(self.plan, q, k, v, gate, beta, out, seq_start, fresh, max_tokens,
+                                           self.state.device), st)
         return out
 
     def save(self, cache, slots, stream=None):
@@ -185,11 +184,18 @@ class DecodeLayer:
     def _slot_index(self, slots):
         return B._index(slots, "slots", self.batch, self.state.device)
 
-    @contextlib.contextmanager
     def _on_device(self, stream):
-        """The layer's device as the current one, and the stream a call runs
-        on there: `stream`, or the device's current stream.  An allocation
-        inside belongs to that stream."""
+        """Context that makes the layer's device current and gives the stream a
+        call runs on there: `stream`, or the device's current stream.  An
+        allocation inside belongs to that stream."""
+        import torch
+        index = self.state.device.index
+        if stream is None and torch.cuda.current_device() == index:
+            return contextlib.nullcontext(torch._C._cuda_getCurrentRawStream(index))
+        return self._switch(stream)
+
+    @contextlib.contextmanager
+    def _switch(self, stream):
         import torch
         with torch.cuda.device(self.state.device):
             if stream is None:
