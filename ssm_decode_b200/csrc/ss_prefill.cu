@@ -16,25 +16,28 @@
 // (g, c) = (lane / 4, lane % 4) holds columns 4c .. 4c+3 of rows 4g .. 4g+3
 // of every 32 (dk / 2 floats).  The eight sums of a token (4 columns, two
 // contractions) are reduced over the 8 row groups by 7 shuffles that halve the
-// number of values each time, and u comes back by 4.  A CTA is the dv / 16
-// warps of a head, or fewer when there are too few heads to fill the SMs.
+// number of values each time, and u comes back by 4.  A CTA is 64 columns of a
+// head, four warps: whole heads (eight warps) left the loads, the tokens and the
+// stores of fewer CTAs to overlap (GDN, 256 x 32 heads, 4 tokens: 248 us against
+// 207), two warps staged k and q too often (KDA prompts 485 against 453 us).
 //
 // What bounds it: for a few tokens the state, read and written once (128 KB a
-// head at 128 x 128); beyond about ten tokens the fp32 pipe, 3 dk dv
-// multiply-adds a token (packed two to an instruction).
+// head at 128 x 128); beyond about ten tokens the fp32 pipe and its issue
+// slots, 3 dk dv multiply-adds a token and KDA's dk dv decays.
 #include "ss_common.cuh"
 
 namespace ss {
 namespace {
 
 constexpr int TOK = 16;                     // tokens staged at a time
+constexpr int VC = 64;                      // state columns of a CTA
 
 // One stage of TOK tokens (bytes): k, q rows, the CTA's columns of v, decays
 // (per channel for KDA), then per token a, b and k . q.
 struct TokLayout {
     int k, q, v, gate, a, b, kq, total;
 };
-__host__ __device__ constexpr TokLayout tok_layout(int fam, int K, int VC) {
+__host__ __device__ constexpr TokLayout tok_layout(int fam, int K) {
     TokLayout L{};
     int o = 0;
     L.k = o; o += TOK * K * 2;
@@ -61,13 +64,14 @@ __device__ __forceinline__ bool seq_rows(const PrefillParams& p, int b, int& fir
 }
 
 template <int FAM, int K>
-__global__ void __launch_bounds__(256) prefill_tokens_kernel(const __grid_constant__ PrefillParams p, int V,
-                                                             int splits) {
+__global__ void __launch_bounds__(2 * VC, K == 128 ? 4 : 6) prefill_tokens_kernel(const __grid_constant__ PrefillParams p,
+                                                                              int V) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int NR = K / 8;                             // state rows of a lane
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, threads = blockDim.x;
-    const int VC = threads >> 1;                          // columns of the CTA: 16 a warp
-    const TokLayout L = tok_layout(FAM, K, VC);
+    constexpr int threads = 2 * VC;
+    constexpr TokLayout L = tok_layout(FAM, K);
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const unsigned splits = unsigned(V) / VC;
     const long long u = blockIdx.x / splits;
     const int col0 = int(blockIdx.x % splits) * VC;
     const int b = int(u / p.H), h = int(u % p.H);
@@ -109,7 +113,7 @@ __global__ void __launch_bounds__(256) prefill_tokens_kernel(const __grid_consta
             cp_async16(sm + L.k + i * 16, gk + r * p.ks + c * 8);
             cp_async16(sm + L.q + i * 16, gq + r * p.qs + c * 8);
         }
-        const int vc = VC / 8;
+        constexpr int vc = VC / 8;
         for (int i = t; i < n * vc; i += threads)
             cp_async16(sm + L.v + i * 16, gv + (r0 + i / vc) * p.vs + (i % vc) * 8);
         if (FAM == KDA) {
@@ -227,14 +231,10 @@ __global__ void __launch_bounds__(256) prefill_tokens_kernel(const __grid_consta
 
 template <int FAM, int K>
 cudaError_t tokens_launch(const PrefillParams& p, int V, cudaStream_t stream) {
-    // As few columns a CTA as still give every SM two CTAs (the state's columns
-    // are independent; each CTA stages the whole keys and queries again).
-    const long long units = (long long)p.B * p.H;
-    int splits = 1;
-    while (splits < V / 16 && units * splits < 2LL * sm_count()) splits *= 2;
-    const int threads = V / 16 / splits * 32;
-    return launch_pdl(prefill_tokens_kernel<FAM, K>, dim3(unsigned(units * splits)), dim3(threads),
-                      2 * tok_layout(FAM, K, threads / 2).total, stream, p, V, splits);
+    const long long ctas = (long long)p.B * p.H * (V / VC);
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    return launch_pdl(prefill_tokens_kernel<FAM, K>, dim3(unsigned(ctas)), dim3(2 * VC), 2 * tok_layout(FAM, K).total, stream,
+                      p, V);
 }
 
 }  // namespace
