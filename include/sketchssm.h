@@ -353,7 +353,12 @@ ss_status ss_step_mixed(ss_plan* plan, const ss_buffers* bufs, const ss_step_io*
  * no rows in the call; their buffered tokens and fill counts stay valid.
  * State, products and sums are fp32; out is rounded once.  Two forms of the
  * same recurrence exist: token by token with the state in registers, and
- * chunks of 64 tokens on the tensor cores. */
+ * (Mamba-2, GDN) chunks of 64 tokens on the tensor cores, which runs from
+ * max_tokens = 32 on (48 with dk or dv = 64, 64 with both); bf16 operands are
+ * cut so that its products are fp32 ones up to 2^-21.  Inputs are expected to
+ * be finite: a NaN or infinity in a token reaches the state and the later
+ * outputs, and in the chunked form it may reach the outputs of the (at most
+ * 63) tokens before it in its chunk, never another sequence. */
 ss_status ss_prefill(ss_plan* plan, const ss_buffers* bufs, const ss_prefill_io* io, ss_stream stream);
 
 /* Bytes of a cache's two buffers for this plan. */
@@ -381,7 +386,8 @@ ss_status ss_traffic_bytes(const ss_plan* plan, int32_t op, int32_t tau, ss_traf
 uint64_t ss_launch_count(void);
 
 /* Testing hook.  With stall != 0 the next launching call of this plan
- * (ss_prime, ss_decode_step, ss_flush, ss_exact_step or ss_replay_step)
+ * (ss_prime, ss_decode_step, ss_flush, ss_exact_step, ss_replay_step, or
+ * ss_prefill in its chunked form; the other form waits for no bulk copies)
  * makes one CTA expect more bytes than its bulk copies deliver, so
  * that CTA's bounded wait runs out after about a second: it sets
  * SS_DEVICE_TIMEOUT in bufs->status and returns, leaving its outputs

@@ -106,6 +106,7 @@ struct PrefillParams {
     int32_t* status;
     long long qs, ks, vs, gs, bs, os;
     int rows, B, H, group, out_bf16;
+    int stall;               // testing hook: extra bytes expected by the first bulk wait (chunked form)
 };
 
 // Parameters of the state cache kernels: `n` values per sequence (H * dk * dv).

@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
             for (int c = 0; c < chunks; ++c) {
                 if (c >= NS && !mbar_wait(freed + s, sph)) { failed = true; break; }
                 const uint32_t qk = smem_u32(sm + L.qk[0] + s * (2 * C * K * 2));
-                mbar_expect_tx(lbar + s, C * (2 * K + V) * 2);
+                mbar_expect_tx(lbar + s, C * (2 * K + V) * 2 + (p.stall && blockIdx.x == 0 && c == 0 ? 16 : 0));
 #pragma unroll
                 for (int j = 0; j < K / 64; ++j) {
                     tma_load_3d(qk + j * (2 * C * 128), &qmap, 64 * j, hq, first + c * C, lbar + s);

@@ -1,8 +1,8 @@
 """GPU parity of ss_prefill against the plain 64-bit recurrence (needs a B200).
 
 Both forms of the call run on the same cases: token by token (max_tokens = 1
-asks for it) and the form the library picks for long sequences (max_tokens =
-the rows).  Lengths from zero on, around the chunk length and odd; sequences
+asks for it) and the form the library picks for long sequences (max_tokens
+far above them).  Lengths from zero on, around the chunk length and odd; sequences
 that start afresh or go on; rows of no sequence, which hold NaN; shared key
 heads, strided rows, both output types; decays of exactly 0 and 1.
 """
@@ -69,7 +69,7 @@ def run_case(family, heads, qk_heads, dk, dv, lengths, fresh, seed, form, out_dt
                      dtype=torch.bfloat16 if out_dtype == "bf16" else torch.float32)
     lay.prefill(dev(d["q"]), dev(d["k"]), dev(d["v"]), dev(d["gate"]),
                 None if family == synth.MAMBA2 else dev(d["beta"]), starts(lengths, first),
-                max_tokens=1 if form == "tokens" else rows, fresh=dev(np.asarray(fresh, np.int32)), out=out)
+                max_tokens=1 if form == "tokens" else 1 << 20, fresh=dev(np.asarray(fresh, np.int32)), out=out)
     torch.cuda.synchronize()
     o, S = out.float().cpu().numpy(), lay.state.cpu().numpy()
     tol = U.tolerance(max(list(lengths) + [1]), dk)
@@ -160,7 +160,7 @@ def test_strided_rows(cuda_ok, family, form):
         else:
             q, k, v, gate, beta = (t[x] for x in ("q", "k", "v", "gate", "beta"))
         lay.prefill(q, k, v, gate, None if family == "mamba2" else beta, starts([n]),
-                    max_tokens=1 if form == "tokens" else n, out=out)
+                    max_tokens=1 if form == "tokens" else 1 << 20, out=out)
         torch.cuda.synchronize()
         if strided:
             assert (wide[:, 0] == 0).all() and (wide[:, 2] == 0).all()
@@ -188,7 +188,7 @@ def test_bad_rows_are_left_out(cuda_ok, table, form):
     lay, state = make_layer(synth.GDN, 3, 2, 64, 64, d["A"], 14)
     out = torch.full((8, 2, 64), 7.0, device="cuda")
     lay.prefill(*(dev(d[x]) for x in ("q", "k", "v", "gate", "beta")), dev(np.asarray(table, np.int32)),
-                max_tokens=1 if form == "tokens" else 8, fresh=dev(np.ones(3, np.int32)), out=out)
+                max_tokens=1 if form == "tokens" else 1 << 20, fresh=dev(np.ones(3, np.int32)), out=out)
     torch.cuda.synchronize()
     assert int(lay.status[0]) == B.SS_DEVICE_BAD_ROWS
     o, S = out.cpu().numpy(), lay.state.cpu().numpy()
@@ -268,7 +268,7 @@ def test_captured_and_on_another_stream(cuda_ok, family, form):
     d = U.draw(fam, sum(lens), H, H, K, V, 16)
     t = [dev(d[x]) for x in ("q", "k", "v", "gate")] + [None if family == "mamba2" else dev(d["beta"])]
     st = starts(lens)
-    mt = 1 if form == "tokens" else sum(lens)
+    mt = 1 if form == "tokens" else 1 << 20
     layers = [make_layer(fam, 2, H, K, V, d["A"], 16)[0] for _ in range(3)]
     outs = [torch.zeros(sum(lens), H, V, device="cuda") for _ in range(3)]
     for _ in range(2):
@@ -285,6 +285,108 @@ def test_captured_and_on_another_stream(cuda_ok, family, form):
     torch.cuda.synchronize()
     for i in (1, 2):
         assert torch.equal(outs[0], outs[i]) and torch.equal(layers[0].state, layers[i].state)
+
+
+@pytest.mark.parametrize("family", ["mamba2", "gdn"])
+def test_more_heads_than_sms_and_many_lengths(cuda_ok, family):
+    """Several units follow one another on an SM; every length modulo the chunk's 64 occurs near its ends."""
+    lens = [1, 62, 63, 64, 65, 66, 126, 128, 130, 191, 192, 193, 0, 40, 320, 257]
+    heads = 11
+    run_case(FAM[family], heads, heads, 64, 64, lens, [i % 3 == 0 for i in range(len(lens))], 18, "long")
+
+
+@pytest.mark.parametrize("form", ["tokens", "long"])
+def test_large_and_small_values(cuda_ok, form):
+    """Values far from one: the split operands keep fp32's relative accuracy over the exponents."""
+    for scale in (2.0 ** 60, 2.0 ** -60):
+        def change(d):
+            d["v"], d["v_"] = U.bf16(d["v_"] * scale)
+        lay, state = make_layer(synth.GDN, 1, 2, 64, 64, np.ones(2, np.float32), 19)
+        state = (state * scale).astype(np.float32)
+        lay.load(state=state)
+        run_case(synth.GDN, 2, 2, 64, 64, [100], [0], 19, form, change=change, layer=(lay, state))
+
+
+@pytest.mark.parametrize("form", ["tokens", "long"])
+def test_row_offsets_beyond_32_bits(cuda_ok, form):
+    """Rows 2^25 elements apart: the last ones lie more than 2^31 elements behind the first."""
+    import torch
+    H, K, n = 2, 64, 70
+    d = U.draw(synth.GDN, n, H, H, K, K, 21)
+    wide = torch.zeros(n << 25, dtype=torch.bfloat16, device="cuda").view(n, 1 << 25)
+    views = []
+    for i, x in enumerate(("q", "k", "v")):
+        view = wide[:, 256 * i:256 * i + H * K].view(n, H, K)
+        view.copy_(dev(d[x]).view(torch.bfloat16))
+        views.append(view)
+    out = wide[:, 1024:1024 + H * K].view(n, H, K)
+    lay, state = make_layer(synth.GDN, 1, H, K, K, d["A"], 21)
+    lay.prefill(*views, dev(d["gate"]), dev(d["beta"]), starts([n]), max_tokens=1 if form == "tokens" else 1 << 20, out=out)
+    torch.cuda.synchronize()
+    ref, ref_S = U.reference(synth.GDN, state, d, [n], [0])
+    check(out.float().cpu().numpy(), ref, U.tolerance(n, K), True)
+    check(lay.state[0].cpu().numpy(), ref_S[0], U.tolerance(n, K))
+
+
+@pytest.mark.parametrize("form", ["tokens", "long"])
+@pytest.mark.parametrize("family", list(FAM))
+def test_nothing_outside_the_buffers_is_written(cuda_ok, family, form):
+    """Canary-padded state, output, slots, status and inputs around ragged calls and a swap."""
+    import torch
+    from tests.test_gpu_canary import Guarded
+    fam, H, lens = FAM[family], 3, [65, 0, 7, 130]
+    for K, V in ((128, 128), (64, 128), (128, 64)):
+        d = U.draw(fam, sum(lens), H, H, K, V, 22)
+        lay, _ = make_layer(fam, 4, H, K, V, d["A"], 22)
+        g = Guarded()
+        for x in ("state", "A", "status"):
+            setattr(lay, x, g.view(getattr(lay, x)))
+        lay._bufs = {w: lay._make_bufs(w) for w in (True, False)}
+        args = [g.view(dev(d[x])) for x in ("q", "k", "v", "gate", "beta")]
+        if family == "mamba2":
+            args[4] = None
+        st, fresh, slots = (g.view(dev(np.asarray(x, np.int32))) for x in (np.cumsum([0] + lens), [0, 1, 0, 1], [2, -1, 0, 1]))
+        for dt in (torch.float32, torch.bfloat16):
+            out = g.view(torch.zeros(sum(lens), H, V, dtype=dt, device="cuda"))
+            lay.prefill(*args, st, max_tokens=1 if form == "tokens" else 1 << 20, fresh=fresh, out=out)
+        for bits in (8, 4):
+            cache = StateCache(lay, 3, bits=bits)
+            cache.codes, cache.scales = g.view(cache.codes), g.view(cache.scales)
+            cache._arg = B.make_cache(cache.codes, cache.scales, 3, bits)
+            lay.save(cache, slots)
+            lay.restore(cache, slots)
+        assert int(lay.status[0]) == 0
+        g.check()
+
+
+@pytest.mark.parametrize("family", ["mamba2", "gdn"])
+def test_wait_that_runs_out(cuda_ok, family):
+    """A copy that one CTA waits for in vain: the call ends, says so, leaves that
+    head's state as it was and completes the others; the next call is sound."""
+    import torch
+    fam, H, lens = FAM[family], 3, [70, 200]
+    d = U.draw(fam, sum(lens), H, H, 64, 64, 20)
+    lay, state = make_layer(fam, 2, H, 64, 64, d["A"], 20)
+    args = [dev(d[x]) for x in ("q", "k", "v", "gate")] + [None if family == "mamba2" else dev(d["beta"]), starts(lens)]
+    B.ss_debug_stall_next_copy(lay.plan)
+    lay.prefill(*args, max_tokens=1 << 20, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert int(lay.status[0]) == B.SS_DEVICE_TIMEOUT
+    _, ref = U.reference(fam, state, d, lens, [0, 0])
+    got = lay.state.cpu().numpy()
+    stalled = [(b, h) for b in range(2) for h in range(H) if (got[b, h] == state[b, h]).all()]
+    assert len(stalled) == 1
+    for b in range(2):
+        for h in range(H):
+            if (b, h) not in stalled:
+                check(got[b, h], ref[b, h], U.tolerance(200, 64))
+    lay.status.zero_()
+    lay.load(state=state)
+    lay.prefill(*args, max_tokens=1 << 20, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert int(lay.status[0]) == 0
+    for b in range(2):
+        check(lay.state[b].cpu().numpy(), ref[b], U.tolerance(200, 64))
 
 
 def test_argument_checks(cuda_ok):
