@@ -7,7 +7,8 @@
 //     U = (I + A)^-1 R,
 //     o_i = g_i S^T q_i + sum_{j<=i} D_ij (q_i . k_j) u_j,
 //     S  <- g_63 S + sum_j k_j (t_j u_j)^T.
-// Mamba-2 has no erase term: A = 0, u_i = dt_i v_i.  With P_ij = D_ij (q_i . k_j),
+// Mamba-2 has no erase term: A = 0, u_i = dt_i v_i, and the outputs' part is
+// (P o dt) V, whose V is exact in bf16 and known from the start.  With P_ij = D_ij (q_i . k_j),
 // U = T R and P U = (P T) R for T = (I + A)^-1, so once S^T k is known one
 // product with the stacked [P T; T] gives the outputs' part and U together.
 // Decays are products of the given a, never ratios or exponentials of sums:
@@ -62,6 +63,8 @@ constexpr int AP = C + 4;                // row pitch of A (floats): float4 rows
 // TMEM columns (all 512).
 constexpr uint32_t T_X = 0;              // [P T; T] R: outputs' part, U; then the state's update (128)
 constexpr uint32_t T_SP = 128;           // S^T in parts (dk / 2 columns each); then R and t o U in parts (32 each)
+constexpr uint32_t T_VP = T_X;           // Mamba-2: v^T in bf16, 16 columns in each half of X (a worker writes
+                                         // where it alone read the last update)
 constexpr uint32_t T_RP = T_SP, T_UP = T_SP + 32 * NP;
 constexpr uint32_t T_D1 = 320;           // S^T q (64), S^T k (64); Mamba-2: the outputs' part in place of S^T k
 constexpr uint32_t T_G = 448;            // Gram products (64)
@@ -218,10 +221,10 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     uint64_t* gread = bars + 10;                               // and read (staging)
     uint64_t* ready = bars + 11;                               // [P T; T] and the decays staged
     uint64_t* sbar = bars + 12;                                // S^T's parts written (workers)
-    uint64_t* rbar = bars + 13;                                // R's parts written (workers)
+    uint64_t* rbar = bars + 13;                                // R's parts, or Mamba-2's v^T, written (workers)
     uint64_t* ubar = bars + 14;                                // t o U's parts written (workers)
     uint64_t* d1bar = bars + 15;                               // D1 done
-    uint64_t* d2bar = bars + 16;                               // [P T; T] R done
+    uint64_t* d2bar = bars + 16;                               // [P T; T] R, or Mamba-2's P v, done
     uint64_t* xbar = bars + 17;                                // the state's update done
     uint64_t* drain = bars + 18;                               // [2] the issuing threads' last MMAs done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
@@ -291,31 +294,48 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 const float4* vg = reinterpret_cast<const float4*>(vec + 2 * C + half * 32);
                 const float4* vt = reinterpret_cast<const float4*>(vec + 3 * C + half * 32);
                 const uint16_t* sv = reinterpret_cast<const uint16_t*>(sm + L.v[0] + s * (C * V * 2)) + half * 32 * V + d;
+                uint32_t vp[16];                               // Mamba-2: v of this thread's tokens, two a register
+                if (!ERASE) {
+                    // (ready first: once the product with v is issued, staging may complete
+                    // the next chunk's, and this one's could no longer be waited for)
+                    if (!warp_wait(lbar + s, sph) || !warp_wait(full + s, sph) || !warp_wait(ready, ph)) { failed = true; break; }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) vp[i] = uint32_t(sv[2 * i * V]) | (uint32_t(sv[(2 * i + 1) * V]) << 16);
+                    tc::st16(tq + T_VP + half * KH, vp);
+                    tc::wait_st();
+                    tc::fence_before();
+                    mbar_arrive(rbar);
+                }
                 put_parts<KH>(tq + T_SP + half * (KH / 2), K / 2, S);
                 tc::wait_st();
                 tc::fence_before();
                 mbar_arrive(sbar);
                 if (c > 0) store(c - 1);
 
-                if (!warp_wait(lbar + s, sph) || !warp_wait(full + s, sph) || !warp_wait(ready, ph) ||
-                    !warp_wait(d1bar, ph)) { failed = true; break; }
+                if (ERASE && (!warp_wait(lbar + s, sph) || !warp_wait(full + s, sph) || !warp_wait(ready, ph))) { failed = true; break; }
+                if (!warp_wait(d1bar, ph)) { failed = true; break; }
                 tc::fence_after();
                 float y[32];
                 if (ERASE) {
                     get<32>(tq + T_D1 + C + half * 32, reinterpret_cast<uint32_t*>(y));
                     tc::wait_ld();
-                }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 bt = vb[i], g = ERASE ? vg[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float be[4] = {bt.x, bt.y, bt.z, bt.w}, ge[4] = {g.x, g.y, g.z, g.w};
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 bt = vb[i], g = vg[i];
+                        const float be[4] = {bt.x, bt.y, bt.z, bt.w}, ge[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = bf2f(sv[(4 * i + e) * V]);
-                        y[4 * i + e] = be[e] * (ERASE ? fmaf(-ge[e], y[4 * i + e], v) : v);
+                        for (int e = 0; e < 4; ++e)
+                            y[4 * i + e] = be[e] * fmaf(-ge[e], y[4 * i + e], bf2f(sv[(4 * i + e) * V]));
+                    }
+                    put_parts<32>(tq + T_RP + half * 16, 32, y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 bt = vb[i];
+                        y[4 * i] = bt.x * bf2f_lo(vp[2 * i]); y[4 * i + 1] = bt.y * bf2f_hi(vp[2 * i]);
+                        y[4 * i + 2] = bt.z * bf2f_lo(vp[2 * i + 1]); y[4 * i + 3] = bt.w * bf2f_hi(vp[2 * i + 1]);
                     }
                 }
-                put_parts<32>(tq + T_RP + half * 16, 32, y);
                 if (ERASE) {
                     tc::wait_st();
                     tc::fence_before();
@@ -337,11 +357,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 mbar_arrive(ubar);
 
                 // the output, beside the update's MMAs
-                if (!ERASE) {
-                    if (!warp_wait(d2bar, ph)) { failed = true; break; }
-                    tc::fence_after();
-                    get<32>(tq + T_D1 + C + half * 32, reinterpret_cast<uint32_t*>(o));
-                }
+                if (!ERASE) get<32>(tq + T_D1 + C + half * 32, reinterpret_cast<uint32_t*>(o));
                 get<32>(tq + T_D1 + half * 32, reinterpret_cast<uint32_t*>(y));
                 tc::wait_ld();
 #pragma unroll
@@ -433,9 +449,15 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 for (int j = C - 4; j >= 0; j -= 4) {          // D_ij from j = i down
                     const float4 a = *reinterpret_cast<const float4*>(vec + j);
                     const float ae[4] = {a.x, a.y, a.z, a.w};
+                    float be[4] = {1.f, 1.f, 1.f, 1.f};
+                    if (!ERASE) {                              // u_j = dt_j v_j: dt goes with P
+                        const float4 bt = *reinterpret_cast<const float4*>(vec + C + j);
+                        be[0] = bt.x; be[1] = bt.y; be[2] = bt.z; be[3] = bt.w;
+                    }
 #pragma unroll
                     for (int e = 3; e >= 0; --e) {
                         x[j + e] = j + e <= row ? dij * x[j + e] : 0.f;
+                        if (!ERASE) x[j + e] *= be[e];
                         if (j + e <= row) dij *= ae[e];
                     }
                 }
@@ -506,34 +528,42 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 // operands further on: the byte distance / 16 added to the address field
                 const uint64_t dqk = tc::sdesc(qk, 16, 1024, tc::LAYOUT_SW128);
                 const uint64_t dkt = tc::sdesc(qk + C * 128, 2 * C * 128, 1024, tc::LAYOUT_SW128);
-                if (!mbar_wait(full + s, sph) || !mbar_wait(sbar, ph)) { failed = true; break; }
-                tc::fence_after();
+                if (!mbar_wait(full + s, sph)) { failed = true; break; }
                 // (rolled loops: unrolled ones keep every operand address in registers the warp does not have)
+                if (!ERASE) {                                  // the outputs' part: v is exact, one part of it
+                    if (!mbar_wait(ready, ph) || !mbar_wait(rbar, ph)) { failed = true; break; }
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int j = 0; j < NP; ++j)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_ts_bf16(tmem + T_D1 + C, tmem + T_VP + (k >> 1) * (K / 2) + (k & 1) * 8,
+                                            dtp + uint32_t(j) * (2 * C * C * 2 >> 4) + 2 * k, id1, j + k > 0);
+                    tc::commit(d2bar);
+                }
+                if (!mbar_wait(sbar, ph)) { failed = true; break; }
+                tc::fence_after();
 #pragma unroll 1
                 for (int i = 0; i < NP * (K / 64); ++i)
                     mma_k64(tmem + T_D1, tmem + T_SP + 32 * i, dqk + uint32_t(i & (K / 64 - 1)) * (2 * C * 128 >> 4), 2, id1,
                             i > 0);
                 tc::commit(d1bar);
-                // [P T; T] R, or Mamba-2's P R beside S^T q
-                auto products = [&](uint32_t dst) {
+                if (ERASE) {
+                    if (!mbar_wait(ready, ph) || !mbar_wait(rbar, ph)) { failed = true; break; }
+                    tc::fence_after();
 #pragma unroll 1
                     for (int i = 0; i < NP; ++i)
 #pragma unroll 1
                         for (int j = 0; i + j < NP; ++j)
-                            mma_k64(dst, tmem + T_RP + 32 * i, dtp + uint32_t(j) * (2 * C * C * 2 >> 4), 2, id1, i + j > 0);
+                            mma_k64(tmem + T_X, tmem + T_RP + 32 * i, dtp + uint32_t(j) * (2 * C * C * 2 >> 4), 2, id1,
+                                    i + j > 0);
                     tc::commit(d2bar);
-                };
-                if (ERASE) {
-                    if (!mbar_wait(ready, ph) || !mbar_wait(rbar, ph)) { failed = true; break; }
-                    tc::fence_after();
-                    products(tmem + T_X);
                 }
-                if (!mbar_wait(ready, ph) || !mbar_wait(ubar, ph)) { failed = true; break; }
+                if (!mbar_wait(ubar, ph)) { failed = true; break; }
                 tc::fence_after();
 #pragma unroll 1
                 for (int i = 0; i < NP; ++i) mma_k64(tmem + T_X, tmem + T_UP + 32 * i, dkt, 2048 >> 4, id3, i > 0);
                 tc::commit(xbar);
-                if (!ERASE) products(tmem + T_D1 + C);
                 tc::commit(freed + s);
                 if (++s == NS) { s = 0; sph ^= 1u; }
             }
