@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     if (p.B > 1 && p.B <= SORT) {
         // CTAs start in order: the b-th longest sequence, so that none of the
         // long ones begins last
-        int* const len = reinterpret_cast<int*>(sm);
+        int* const len = reinterpret_cast<int*>(sm + L.a);     // (no copy lands here)
         if (t < p.B) len[t] = p.seq_start[t + 1] - p.seq_start[t];
         __syncthreads();
         int rank = 0;
@@ -589,7 +589,8 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
             const int hq = h / p.group;
             int s = 0;
             unsigned sph = 1;
-            for (int c = 0; c < chunks; ++c) {
+            int c = 0;
+            for (; c < chunks; ++c) {
                 if (c >= NS && !mbar_wait(freed + s, sph)) { failed = true; break; }
                 const uint32_t qk = smem_u32(sm + L.qk[0] + s * (2 * C * K * 2));
                 mbar_expect_tx(lbar + s, C * (2 * K + V) * 2 + (p.stall && blockIdx.x == 0 && c == 0 ? 16 : 0));
@@ -601,6 +602,10 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
                 tma_load_3d(smem_u32(sm + L.v[0] + s * (C * V * 2)), &vmap, 0, h, first + c * C, lbar + s);
                 if (++s == NS) { s = 0; sph ^= 1u; }
             }
+            // nothing is in flight into this CTA's shared memory when it ends (they
+            // have long been waited for, unless a wait ran out)
+            for (int i = max(0, c - NS); i < c; ++i)
+                if (!mbar_wait(lbar + i % NS, (i / NS) & 1)) failed = true;
         } else if (warp == NWK / 32 + 6) {
             // -------------------------------------------------------- Gram products
             constexpr uint32_t id = tc::idesc_bf16(128, C);

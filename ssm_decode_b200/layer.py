@@ -151,7 +151,7 @@ class DecodeLayer:
         (device int32 [batch + 1]).  Rows may be strided, and qk_heads may
         divide heads (shared keys).  max_tokens (a host int, at least the
         longest sequence) lets the library pick the faster form; None takes
-        the number of rows.  Returns out [rows][heads][dv], allocated in
+        the number of rows, so give it for short drafts of many sequences.  Returns out [rows][heads][dv], allocated in
         `out_dtype` (bf16 unless given) when not passed; rows of no sequence
         are left as they were (zero in an allocated one).  Needs phase 0;
         prime() comes before the next sketched step."""

@@ -168,6 +168,47 @@ def test_strided_rows(cuda_ok, family, form):
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
+def test_another_current_device_or_stream_handle(cuda_ok):
+    """A raw stream handle (0: the default stream) and an allocated output, under another stream's context."""
+    import torch
+    d = U.draw(synth.GDN, 40, 2, 2, 64, 64, 23)
+    args = [dev(d[x]) for x in ("q", "k", "v", "gate", "beta")] + [starts([40])]
+    outs = []
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (None, 0, side.cuda_stream, side):
+        lay, _ = make_layer(synth.GDN, 1, 2, 64, 64, d["A"], 23)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            outs.append((lay.prefill(*args, stream=handle), lay))
+        torch.cuda.synchronize()
+    assert all(torch.equal(outs[0][0], o) and torch.equal(outs[0][1].state, lay.state) for o, lay in outs)
+    assert outs[0][0].dtype == torch.bfloat16
+
+
+@pytest.mark.parametrize("family", list(FAM))
+def test_no_token_reaches_another_sequence(cuda_ok, family):
+    """A sequence of NaN and infinities between two others in the same chunk's rows leaves them bit for bit as without it."""
+    import torch
+    fam, H, K, V, lens = FAM[family], 2, 64, 128, [70, 20, 75]
+    d = U.draw(fam, sum(lens), H, H, K, V, 24)
+    got = []
+    for bad in (False, True):
+        t = {x: dev(d[x]) for x in ("q", "k", "v", "gate", "beta")}
+        if bad:
+            for x in ("q", "k", "v"):
+                t[x][70:90] = 0x7F80                       # infinity
+            t["gate"][70:90] = float("nan")
+        for form in (1, 1 << 20):
+            lay, _ = make_layer(fam, 3, H, K, V, d["A"], 24)
+            out = lay.prefill(*(t[x] for x in ("q", "k", "v", "gate")), None if family == "mamba2" else t["beta"], starts(lens),
+                              max_tokens=form)
+            torch.cuda.synchronize()
+            got.append((out[:70].cpu(), out[90:].cpu(), lay.state[0].cpu(), lay.state[2].cpu()))
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], got[i + 2]))
+
+
 def test_no_rows(cuda_ok):
     import torch
     lay, state = make_layer(synth.GDN, 3, 2, 64, 64, np.ones(2, np.float32), 13)
