@@ -57,9 +57,17 @@ __device__ __forceinline__ uint16_t quantise4(const float (&f)[4], unsigned a, u
     constexpr float M = BITS == 8 ? 127.f : 7.f;
     constexpr float MAGIC = 12582912.f;                    // 1.5 * 2^23: x + MAGIC holds rint(x) in its low bits
     const bool finite = a < 0x7f800000u;
-    const uint16_t sb = finite ? f2bf(__fdiv_rn(__uint_as_float(a), M)) : uint16_t(0x7fc0);
+    // top / M rounded to fp32: one step of correction after the product with
+    // 1 / M, right for all 2^23 mantissas (tried one by one) wherever the
+    // remainder, 2^-24 of top, is a normal number
+    const float top = __uint_as_float(a);
+    float d = top * (1.f / M);
+    d = fmaf(fmaf(-d, M, top), 1.f / M, d);
+    if (top < 7.9e-31f) d = __fdiv_rn(top, M);
+    const uint16_t sb = finite ? f2bf(d) : uint16_t(0x7fc0);
     const float scale = bf2f(sb);
-    const float inv = __frcp_rn(scale);
+    float inv;                                             // within two units in the last place
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
     float worst = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -117,7 +125,9 @@ __global__ void __launch_bounds__(CT) cache_write_kernel(const __grid_constant__
                 const unsigned w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
                 *reinterpret_cast<unsigned*>(static_cast<uint8_t*>(p.codes) + v) = w;
             } else {
-                const unsigned w = (c[0] & 15) | ((c[1] & 15) << 4) | ((c[2] & 15) << 8) | ((c[3] & 15) << 12);
+                unsigned w = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410) & 0x0f0f0f0fu;
+                w = (w | (w >> 4));                        // bytes 0 and 2: codes 1 | 0 and 3 | 2
+                w = (w & 0xffu) | ((w >> 8) & 0xff00u);
                 *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.codes) + v / 2) = uint16_t(w);
             }
             if ((threadIdx.x & 7) == 0) p.scales[v / 32] = sb;
