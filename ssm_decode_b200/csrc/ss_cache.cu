@@ -13,11 +13,10 @@
 // it), so |r| against scale / 2 decides, and a tie goes to the even code.
 //
 // What bounds them: the bytes, 4 + bits/8 + 1/16 a value, one pass.  537 MB of
-// state at 8 bits: save 117 us, restore 113 us (floor 104 us at the measured copy
-// rate); at 4 bits 121 and 102 us (floor 93 us), the save's integer work then
-// keeping its issue slots busy (79 % at 8 bits).  A CTA takes up to four chunks
-// and fetches one ahead: one chunk a CTA spent its time on the slot's latency
-// (147 us each way).
+// state at 8 bits: save 113 us, restore 114 us (floor 104 us at the measured copy
+// rate); at 4 bits 111 and 102 us (floor 93 us), the save's integer work then
+// being next.  A CTA takes up to four chunks and fetches one ahead: one chunk a
+// CTA spent its time on the slot's latency (147 us each way).
 #include "ss_common.cuh"
 
 namespace ss {

@@ -53,7 +53,7 @@
 // straight-line code at about four cycles an instruction, instruction fetches
 // being the largest stall after the waits; the tensor pipe is active 30 % of the
 // time (60 MMAs of 77 cycles, whatever N up to 128, and the Gram products).
-// 8192 tokens x 32 heads take 686 us (32 of 148 SMs), 16 x 1024 tokens 438 us.
+// 8192 tokens x 32 heads take 700 us (32 of 148 SMs), 16 x 1024 tokens 438 us.
 // Measured and left out: the inverse by 16 x 16 blocks (fp32 tiles 400 against
 // 350 us for 4096 tokens x 32 heads; warp-level tf32 or bf16 MMAs wait for the
 // tcgen05 ones, 400 cycles and more a block), 8 staging or 16 worker warps

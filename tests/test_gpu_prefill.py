@@ -299,6 +299,49 @@ def test_prompt_in_parts_then_decode(cuda_ok, family):
     assert int(lay.status[0]) == 0
 
 
+@pytest.mark.parametrize("family", list(FAM))
+def test_new_sequence_joins_a_mixed_batch(cuda_ok, family):
+    """Continuous batching: while sequence 0 sits inside its window, sequence 1
+    ends and a new prompt takes its place; after prime() both go on, sequence 0
+    with the tokens it had buffered (ranks = dk: the sketch is exact)."""
+    import torch
+    fam, H, K, V, W, n = FAM[family], 2, 64, 64, 4, 40
+    d = U.draw(fam, 2 * 7 + n, H, H, K, V, 25)
+    lay = DecodeLayer(fam, 2, H, K, V, W, [K] * H)
+    eye = np.concatenate([np.eye(K, dtype=np.float32)] * H)
+    S = np.random.default_rng(25).standard_normal((2, H, K, V)).astype(np.float32) * 0.3
+    lay.load(state=S, basis=eye, coef=eye, A=d["A"])
+    S = S.astype(np.float64)
+    fills = [torch.zeros(2, dtype=torch.int32, device="cuda") for _ in range(2)]
+    cut = lambda a, b: {x: d[x][a:b] for x in ("q", "k", "v", "gate", "beta", "q_", "k_", "v_")}  # noqa: E731
+
+    def steps(at, count):
+        for i in range(count):
+            c = cut(at + 2 * i, at + 2 * i + 2)
+            lay.step_mixed(lay.token({x: c[x] for x in ("q", "k", "v", "gate", "beta")}), *fills)
+            torch.cuda.synchronize()
+            fills.reverse()
+            for b in range(2):
+                one = {x: c[x][b:b + 1] for x in c}
+                ref, S_b = U.reference(fam, S[b:b + 1], {**one, "A": d["A"]}, [1], [0])
+                S[b] = S_b[0]
+                check(lay.out[b].cpu().numpy(), ref[0], 1e-4)
+
+    lay.prime()
+    steps(0, 2)
+    c = cut(4, 4 + n)
+    out = lay.prefill(*(dev(c[x]) for x in ("q", "k", "v", "gate")), None if family == "mamba2" else dev(c["beta"]),
+                      starts([0, n]), max_tokens=n, fresh=dev(np.asarray([0, 1], np.int32)), out_dtype=torch.float32)
+    ref, S_1 = U.reference(fam, S[1:2], {**c, "A": d["A"]}, [n], [1])
+    S[1] = S_1[0]
+    torch.cuda.synchronize()
+    check(out.cpu().numpy(), ref, U.tolerance(n, K))
+    fills[0][1] = 0
+    lay.prime()
+    steps(4 + n, 5)
+    assert fills[0].tolist() == [3, 1] and int(lay.status[0]) == 0
+
+
 @pytest.mark.parametrize("form", ["tokens", "long"])
 @pytest.mark.parametrize("family", list(FAM))
 def test_captured_and_on_another_stream(cuda_ok, family, form):
