@@ -106,8 +106,12 @@ struct PrefillParams {
     int32_t* status;
     long long qs, ks, vs, gs, bs, os;
     int rows, B, H, group, out_bf16;
+    int order;               // chunked form: the sequences longest first (B <= PREFILL_ORDER_MAX), those without
+                             // tokens not at all
     int stall;               // testing hook: extra bytes expected by the first bulk wait (chunked form)
 };
+
+constexpr int PREFILL_ORDER_MAX = 512;     // largest batch with PrefillParams::order
 
 // Parameters of the state cache kernels: `n` values per sequence (H * dk * dv).
 struct CacheParams {

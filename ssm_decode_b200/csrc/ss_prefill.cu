@@ -24,7 +24,7 @@
 // What bounds it: for a few tokens the state, read and written once (128 KB a
 // head at 128 x 128); beyond about ten tokens the fp32 pipe and its issue
 // slots, 3 dk dv multiply-adds a token and KDA's dk dv decays.
-#include "ss_common.cuh"
+#include "ss_prefill.cuh"
 
 namespace ss {
 namespace {
@@ -51,18 +51,6 @@ __host__ __device__ constexpr TokLayout tok_layout(int fam, int K) {
     return L;
 }
 
-// The row range of sequence b; false (and the status bit) if it is not a range of the call's rows.
-__device__ __forceinline__ bool seq_rows(const PrefillParams& p, int b, int& first, int& count) {
-    const int s = p.seq_start[b], e = p.seq_start[b + 1];
-    if (s < 0 || e < s || e > p.rows) {
-        if (threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
-        return false;
-    }
-    first = s;
-    count = e - s;
-    return true;
-}
-
 template <int FAM, int K>
 __global__ void __launch_bounds__(2 * VC, K == 128 ? 4 : 6) prefill_tokens_kernel(const __grid_constant__ PrefillParams p,
                                                                               int V) {
@@ -78,7 +66,10 @@ __global__ void __launch_bounds__(2 * VC, K == 128 ? 4 : 6) prefill_tokens_kerne
     griddep_wait();
     griddep_launch_next();
     int first, count;
-    if (!seq_rows(p, b, first, count)) return;
+    if (!seq_rows(p, b, first, count)) {
+        if (t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
+        return;
+    }
     const bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
     if (count == 0 && !fresh) return;
 

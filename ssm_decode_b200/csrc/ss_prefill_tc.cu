@@ -60,6 +60,7 @@
 // (fewer registers a thread: spills, and with the SM's shared memory in use they
 // miss L1), persistent CTAs (391 us), S handed over in two steps (373 us).
 #include "ss_mma.cuh"
+#include "ss_prefill.cuh"
 #include "ss_tc.cuh"
 
 namespace ss {
@@ -71,7 +72,6 @@ constexpr int NWK = 256;                 // worker threads
 constexpr int NST = 128;                 // staging threads
 constexpr int NT = NWK + NST + 128;
 constexpr int NS = 3;                    // stages of q, k, v
-constexpr int SORT = 256;                // up to so many sequences are taken longest first
 constexpr int AP = C + 4;                // row pitch of A (floats): float4 rows without bank conflicts
 
 // TMEM columns (all 512).
@@ -196,35 +196,23 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     griddep_wait();
     griddep_launch_next();
     const int h = int(blockIdx.x % unsigned(p.H));
-    int b = int(blockIdx.x / unsigned(p.H));
-    if (p.B > 1 && p.B <= SORT) {
-        // CTAs start in order: the b-th longest sequence, so that none of the
-        // long ones begins last
-        int* const len = reinterpret_cast<int*>(sm + L.a);     // (no copy lands here)
-        if (t < p.B) len[t] = p.seq_start[t + 1] - p.seq_start[t];
-        __syncthreads();
-        int rank = 0;
-        if (t < p.B)
-            for (int j = 0; j < p.B; ++j) rank += len[j] > len[t] || (len[j] == len[t] && j < t);
-        __syncthreads();
-        if (t < p.B && rank == b) len[0] = t;
-        __syncthreads();
-        b = len[0];
-        __syncthreads();
+    int b = int(blockIdx.x / unsigned(p.H)), first, count;
+    const bool good = seq_rows(p, b, first, count);
+    if (!good && t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
+    bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
+    if (good && count == 0 && fresh) {                         // no token: the state only starts afresh
+        float4* const s0 = reinterpret_cast<float4*>(p.state + ((long long)b * p.H + h) * (K * V));
+        for (int i = t; i < K * V / 4; i += NT) s0[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int first = p.seq_start[b], end = p.seq_start[b + 1];
-    if (first < 0 || end < first || end > p.rows) {
-        if (t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
+    if (p.order) {
+        b = sequence_at<NT>(p, b, reinterpret_cast<int*>(sm + L.a));     // (no copy lands in this scratch)
+        if (b < 0 || !seq_rows(p, b, first, count)) return;
+        fresh = p.fresh != nullptr && p.fresh[b] != 0;
+    } else if (!good) {
         return;
     }
-    const int count = end - first;
-    const bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
+    if (count == 0) return;
     float* const state = p.state + ((long long)b * p.H + h) * (K * V);
-    if (count == 0) {
-        if (fresh)
-            for (int i = t; i < K * V / 4; i += NT) reinterpret_cast<float4*>(state)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        return;
-    }
     const int chunks = (count + C - 1) / C;
 
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L.bars);

@@ -380,6 +380,17 @@ def test_more_heads_than_sms_and_many_lengths(cuda_ok, family):
 
 
 @pytest.mark.parametrize("form", ["tokens", "long"])
+@pytest.mark.parametrize("batch", [200, 512, 600])
+def test_few_sequences_of_a_large_batch(cuda_ok, batch, form):
+    """Prompts for a few places of a large batch (put in order up to 512 sequences): the others keep their state or start afresh."""
+    r = np.random.default_rng(batch)
+    lens = np.zeros(batch, int)
+    lens[r.choice(batch, 9, replace=False)] = [1, 70, 5, 70, 64, 130, 2, 33, 70]
+    lens[-1] = 3
+    run_case(synth.GDN, 2, 1, 64, 64, lens.tolist(), (r.random(batch) < 0.5).astype(int).tolist(), 26, form, first=1)
+
+
+@pytest.mark.parametrize("form", ["tokens", "long"])
 def test_large_and_small_values(cuda_ok, form):
     """Values far from one: the split operands keep fp32's relative accuracy over the exponents."""
     for scale in (2.0 ** 60, 2.0 ** -60):
