@@ -620,9 +620,8 @@ ss_status ss_prefill(ss_plan* pl, const ss_buffers* b, const ss_prefill_io* io, 
     const bool chunks = !kda && io->rows > 0 && longest >= chunk_tokens(c);
     const int stall = take_stall(pl);
     p.stall = chunks && stall;
-    // worth its start-up (a microsecond or two a block) where many sequences are
-    // much shorter than the longest
-    p.order = c.batch > 1 && c.batch <= ss::PREFILL_ORDER_MAX && io->rows * 4 < int64_t(c.batch) * 3 * longest;
+    // (sequences of much the same length too: two rounds of them then end together)
+    p.order = c.batch > 1 && c.batch <= ss::PREFILL_ORDER_MAX;
     CHECK(launch_via(pl, "prefill", [&] {
         if (chunks)
             return ss::launch_prefill_chunks(c.family, c.dk, c.dv, p, reinterpret_cast<cudaStream_t>(stream));
