@@ -194,7 +194,12 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     constexpr bool ERASE = FAM == GDN;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     griddep_wait();
-    griddep_launch_next();
+    // The next launch is let in when this one ends, not here: its blocks would
+    // settle one by one on the SMs that fall idle first, long sequences beside
+    // short ones, and the two SMs of a pair, which share instruction fetches, take
+    // 5.5 to 6.9 us a chunk in step and 7 to 9 us apart.  16 ragged sequences x 32
+    // heads, calls back to back: 512 us with the early start, 428 without it (432
+    // with another kernel between); equal lengths lose nothing (237 and 237 us).
     const int h = int(blockIdx.x % unsigned(p.H));
     int b = int(blockIdx.x / unsigned(p.H)), first, count;
     const bool good = seq_rows(p, b, first, count);

@@ -1,0 +1,39 @@
+"""Speed that is lost by how calls follow one another, not by the work in them (needs a B200)."""
+import numpy as np
+import pytest
+
+from ssm_decode_b200 import synth
+from ssm_decode_b200.layer import DecodeLayer
+from tests import many_token_util as U
+from tests.test_gpu_prefill import dev, starts
+
+pytestmark = pytest.mark.gpu
+
+
+def test_ragged_calls_back_to_back(cuda_ok):
+    """Calls of a ragged batch, one right behind the other, take no longer than with another kernel between them:
+    the next call's blocks do not settle among the last ones of the call before.  (Before they were kept out the
+    first way took 1.18 times the second; without, 0.99.)"""
+    import torch
+    lens = [4096, 3689, 1867, 1477, 1458, 1202, 934, 868, 232, 44, 35, 16, 4, 2, 1, 1]
+    H, D = 32, 128
+    d = U.draw(synth.GDN, sum(lens), H, 1, D, D, 30)
+    lay = DecodeLayer(synth.GDN, len(lens), H, D, D, 4, [2] * H)
+    args = [dev(d[x]) for x in ("q", "k", "v", "gate", "beta")] + [starts(lens)]
+    out = torch.zeros(sum(lens), H, D, device="cuda")
+    small = torch.zeros(32, device="cuda")
+
+    def time(between):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(20):
+            lay.prefill(*args, max_tokens=max(lens), out=out)
+            if between:
+                small.add_(1)
+        b.record()
+        b.synchronize()
+        return a.elapsed_time(b) / 20
+
+    time(False), time(True)
+    t = np.array([[time(False), time(True)] for _ in range(8)]).min(0)
+    assert t[0] <= 1.08 * t[1], f"{t[0] * 1e3:.0f} us back to back, {t[1] * 1e3:.0f} us with a kernel between"
