@@ -387,9 +387,9 @@ uint64_t ss_launch_count(void);
 
 /* Testing hook.  With stall != 0 the next launching call of this plan
  * (ss_prime, ss_decode_step, ss_flush, ss_exact_step, ss_replay_step, or
- * ss_prefill in its chunked form; the other form waits for no bulk copies)
- * makes one CTA expect more bytes than its bulk copies deliver, so
- * that CTA's bounded wait runs out after about a second: it sets
+ * ss_prefill in its chunked form; its other form and the state cache calls
+ * wait for no bulk copies and leave the hook armed) makes one CTA expect
+ * more bytes than its bulk copies deliver, so that CTA's bounded wait runs out after about a second: it sets
  * SS_DEVICE_TIMEOUT in bufs->status and returns, leaving its outputs
  * incomplete; the rest of the launch completes.  The hook clears itself
  * after that call.  Used to test the timeout path without a device fault. */

@@ -618,8 +618,7 @@ ss_status ss_prefill(ss_plan* pl, const ss_buffers* b, const ss_prefill_io* io, 
     p.out_bf16 = io->out_dtype == SS_BF16;
     const int64_t longest = io->max_tokens == 0 ? io->rows : io->max_tokens;
     const bool chunks = !kda && io->rows > 0 && longest >= chunk_tokens(c);
-    const int stall = take_stall(pl);
-    p.stall = chunks && stall;
+    p.stall = chunks ? take_stall(pl) : 0;       // (the token form has no bulk copies: the hook stays armed)
     // (sequences of much the same length too: two rounds of them then end together)
     p.order = c.batch > 1 && c.batch <= ss::PREFILL_ORDER_MAX;
     CHECK(launch_via(pl, "prefill", [&] {

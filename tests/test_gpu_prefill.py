@@ -484,6 +484,28 @@ def test_wait_that_runs_out(cuda_ok, family):
         check(lay.state[b].cpu().numpy(), ref[b], U.tolerance(200, 64))
 
 
+def test_stall_hook_waits_for_a_call_with_bulk_copies(cuda_ok):
+    """The testing hook stays armed over calls that wait for no bulk copy."""
+    import torch
+    d = U.draw(synth.GDN, 70, 2, 2, 64, 64, 27)
+    lay, _ = make_layer(synth.GDN, 1, 2, 64, 64, d["A"], 27)
+    args = [dev(d[x]) for x in ("q", "k", "v", "gate", "beta")] + [starts([70])]
+    cache, slots = StateCache(lay, 1), dev(np.zeros(1, np.int32))
+    B.ss_debug_stall_next_copy(lay.plan)
+    lay.prefill(*args, max_tokens=1)
+    lay.save(cache, slots)
+    lay.restore(cache, slots)
+    torch.cuda.synchronize()
+    assert int(lay.status[0]) == 0
+    lay.prefill(*args, max_tokens=1 << 20)
+    torch.cuda.synchronize()
+    assert int(lay.status[0]) == B.SS_DEVICE_TIMEOUT
+    lay.status.zero_()
+    lay.prefill(*args, max_tokens=1 << 20)
+    torch.cuda.synchronize()
+    assert int(lay.status[0]) == 0
+
+
 def test_argument_checks(cuda_ok):
     import torch
     lay, _ = make_layer(synth.GDN, 2, 4, 64, 64, np.ones(4, np.float32), 17)
