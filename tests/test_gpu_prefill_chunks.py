@@ -1,4 +1,4 @@
-"""The chunked form of ss_prefill: the bits its operand splits keep (needs a B200)."""
+"""The chunked form of ss_prefill: the bits its operand splits keep, and long prompts (needs a B200)."""
 import numpy as np
 import pytest
 
@@ -6,7 +6,7 @@ from ssm_decode_b200 import synth
 from ssm_decode_b200.layer import DecodeLayer
 from tests import chunk_cases as cases
 from tests import many_token_util as U
-from tests.test_gpu_prefill import dev, starts
+from tests.test_gpu_prefill import check, dev, make_layer, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,44 @@ def test_split_operands_keep_every_bit(cuda_ok, family, form, lead, dk, dv):
             off = np.abs(got.astype(np.float64) - want)
             assert (off <= room).all(), f"{name}, {what}: {(off > room).sum()} beyond the room, {(off - room).max():.2e} at most"
         assert int(lay.status[0]) == 0
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (128, 64)])
+@pytest.mark.parametrize("family", list(FAM))
+def test_long_prompts(cuda_ok, family, dk, dv):
+    """65 chunks beside shorter prompts, against 64 bits.  The decays over 64 tokens are below 2^-10, so an error
+    more than a chunk old no longer counts: the tolerance is that of 128 tokens."""
+    import torch
+    fam, H, lens = FAM[family], 2, [4133, 1, 2048, 1000]
+    d = U.draw(fam, sum(lens), H, 1, dk, dv, 31)
+    a = np.exp(d["gate"] * d["A"]) if family == "mamba2" else d["gate"]
+    g = np.cumsum(np.log(a.astype(np.float64)), 0)
+    assert (g[64:] - g[:-64]).max() < np.log(2.0 ** -10)
+    lay, state = make_layer(fam, len(lens), H, dk, dv, d["A"], 31)
+    out = lay.prefill(*(dev(d[x]) for x in ("q", "k", "v", "gate")), None if family == "mamba2" else dev(d["beta"]), starts(lens),
+                      max_tokens=max(lens), out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    ref, ref_S = U.reference(fam, state, d, lens, [0] * len(lens))
+    tol = U.tolerance(128, dk) * (1 + 2.0 ** -9)
+    for h in range(H):
+        check(out[:, h].cpu().numpy(), ref[:, h], tol)
+    for b in range(len(lens)):
+        check(lay.state[b].cpu().numpy(), ref_S[b], tol)
+
+
+@pytest.mark.parametrize("family", list(FAM))
+def test_a_prompt_in_parts_of_whole_chunks_is_the_same_bits(cuda_ok, family):
+    """2500 tokens in one call and in three, cut between chunks: the state handed over is the one the kernel kept."""
+    import torch
+    fam, H, K, V, n = FAM[family], 3, 128, 128, 2500
+    d = U.draw(fam, n, H, H, K, V, 32)
+    args = [dev(d[x]) for x in ("q", "k", "v", "gate")] + [None if family == "mamba2" else dev(d["beta"])]
+    got = []
+    for cuts in ([0, n], [0, 64 * 13, 64 * 14, n]):
+        lay, _ = make_layer(fam, 1, H, K, V, d["A"], 32)
+        out = torch.zeros(n, H, V, device="cuda")
+        for s, e in zip(cuts, cuts[1:]):
+            lay.prefill(*args, dev(np.asarray([s, e], np.int32)), max_tokens=n, out=out)
+        torch.cuda.synchronize()
+        got.append((out.cpu(), lay.state.cpu()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
