@@ -140,13 +140,19 @@ class ClockSampler:
 # ---------------------------------------------------------------------------
 # our arm
 # ---------------------------------------------------------------------------
+# Sources none of whose code is in the kernels timed here: the host-only API file
+# and the kernels of the many-token and state cache calls.  A file that is not
+# named counts.
+OTHER_SOURCES = ("ss_api.cu", "ss_many.h", "ss_prefill.cu", "ss_prefill.cuh", "ss_prefill_tc.cu", "ss_cache.cu")
+
+
 def kernel_source_sha():
-    """Hash of the device-code sources (every CUDA source but the host-only
-    API file), to tell whether ncu counters are still current."""
+    """Hash of the device-code sources that the timed kernels are built from,
+    to tell whether ncu counters are still current."""
     d = os.path.join(ROOT, "ssm_decode_b200", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):
-        if f == "ss_api.cu":
+        if f in OTHER_SOURCES:
             continue
         with open(os.path.join(d, f), "rb") as fh:
             h.update(f.encode() + fh.read())

@@ -9,6 +9,7 @@
 #include <string>
 
 #include "ss_internal.h"
+#include "ss_many.h"
 
 namespace ss {
 int flush_smem_bytes(int family, int dk, int dv, int n, int rpad, bool smap);

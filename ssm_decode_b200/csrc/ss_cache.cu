@@ -18,6 +18,7 @@
 // being next.  A CTA takes up to four chunks and fetches one ahead: one chunk a
 // CTA spent its time on the slot's latency (147 us each way).
 #include "ss_common.cuh"
+#include "ss_many.h"
 
 namespace ss {
 namespace {

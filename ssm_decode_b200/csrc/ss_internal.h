@@ -90,40 +90,6 @@ struct StepParams {
     int off[SS_MAX_HEADS + 1];
 };
 
-// Parameters of the many-token kernels (ss_prefill).  Strides are elements
-// between token rows; head h reads q and k of head h / group.
-struct PrefillParams {
-    float* state;
-    const float* A;
-    const uint16_t* q;
-    const uint16_t* k;
-    const uint16_t* v;
-    const float* gate;
-    const float* beta;
-    void* out;
-    const int32_t* seq_start;
-    const int32_t* fresh;
-    int32_t* status;
-    long long qs, ks, vs, gs, bs, os;
-    int rows, B, H, group, out_bf16;
-    int order;               // chunked form: the sequences longest first (B <= PREFILL_ORDER_MAX), those without
-                             // tokens not at all
-    int stall;               // testing hook: extra bytes expected by the first bulk wait (chunked form)
-};
-
-constexpr int PREFILL_ORDER_MAX = 512;     // largest batch with PrefillParams::order
-
-// Parameters of the state cache kernels: `n` values per sequence (H * dk * dv).
-struct CacheParams {
-    float* state;
-    void* codes;
-    uint16_t* scales;
-    const int32_t* slot;     // [B], < 0: the sequence is left out
-    int32_t* status;
-    long long n;
-    int B, slots;
-};
-
 __host__ __device__ inline bool head_dense(const uint32_t* mask, int h) { return (mask[h >> 5] >> (h & 31)) & 1u; }
 
 // Launchers return the launch's cudaError_t (cudaSuccess when queued).
@@ -144,13 +110,5 @@ cudaError_t launch_decode(int family, int dk, int dv, const StepParams& p, int r
                           cudaStream_t stream);
 cudaError_t launch_replay(int family, int dk, int dv, const StepParams& p,
                           cudaStream_t stream);
-
-// Many tokens per sequence, token by token with the state in registers.
-cudaError_t launch_prefill_tokens(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream);
-// The same in chunks of 64 tokens on the tensor cores (Mamba-2, GDN).
-cudaError_t launch_prefill_chunks(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream);
-// States into / out of quantised slots.
-cudaError_t launch_cache_write(int bits, const CacheParams& p, cudaStream_t stream);
-cudaError_t launch_cache_read(int bits, const CacheParams& p, cudaStream_t stream);
 
 }  // namespace ss

@@ -2,6 +2,7 @@
 // order in which the chunked form runs them.
 #pragma once
 #include "ss_common.cuh"
+#include "ss_many.h"
 
 namespace ss {
 

@@ -82,6 +82,29 @@ def test_kernel_source_sha_ignores_the_host_api_file(tmp_path, monkeypatch):
     assert bench.kernel_source_sha() != a
 
 
+def test_kernel_source_sha_ignores_kernels_that_are_not_timed(tmp_path, monkeypatch):
+    """A change to the many-token or state cache kernels leaves the traffic records of decode and flush current; no
+    timed kernel's source includes or defines what is left out."""
+    import shutil
+    real = os.path.join(bench.ROOT, "ssm_decode_b200", "csrc")
+    csrc = tmp_path / "ssm_decode_b200" / "csrc"
+    shutil.copytree(real, csrc)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    a = bench.kernel_source_sha()
+    for f in ("ss_many.h", "ss_prefill.cu", "ss_prefill.cuh", "ss_prefill_tc.cu", "ss_cache.cu"):
+        (csrc / f).write_text((csrc / f).read_text() + "// changed\n")
+        assert bench.kernel_source_sha() == a, f
+    for f in sorted(os.listdir(csrc)):
+        if f in bench.OTHER_SOURCES:
+            continue
+        text = (csrc / f).read_text()
+        assert not any(f'#include "{o}"' in text for o in bench.OTHER_SOURCES), f
+        (csrc / f).write_text(text + "// changed\n")
+        assert bench.kernel_source_sha() != a, f
+        (csrc / f).write_text(text)
+    assert bench.kernel_source_sha() == a
+
+
 def test_cpu_baseline_all_cores_leg_and_its_fallback():
     """The oracle baseline: a 1-thread figure, then single-threaded spawned
     processes whose rates add up; a parallel leg that fails or runs out of
