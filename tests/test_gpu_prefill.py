@@ -186,6 +186,30 @@ def test_another_current_device_or_stream_handle(cuda_ok):
     assert outs[0][0].dtype == torch.bfloat16
 
 
+def test_a_layer_on_a_device_that_is_not_current(cuda_ok):
+    """prefill in both forms, save and restore on the second device while the first is current, against the first."""
+    import torch
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two devices")
+    d = U.draw(synth.GDN, 90, 2, 2, 64, 64, 28)
+    got = []
+    for device, stream in (("cuda:0", None), ("cuda:1", None), ("cuda:1", torch.cuda.Stream("cuda:1"))):
+        lay = DecodeLayer(synth.GDN, 1, 2, 64, 64, 4, [2] * 2, device=torch.device(device))
+        cache = StateCache(lay, 1)
+        args = [dev(d[x]).to(device) for x in ("q", "k", "v", "gate", "beta")] + [starts([90]).to(device)]
+        slots = torch.zeros(1, dtype=torch.int32, device=device)
+        torch.cuda.synchronize(device)
+        assert torch.cuda.current_device() == 0
+        outs = [lay.prefill(*args, max_tokens=1, stream=stream), lay.prefill(*args, max_tokens=1 << 20, stream=stream)]
+        lay.save(cache, slots, stream=stream)
+        lay.restore(cache, slots, stream=stream)
+        torch.cuda.synchronize(device)
+        assert int(lay.status[0]) == 0
+        got.append([x.cpu() for x in outs + [lay.state, cache.codes, cache.scales]])
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
 @pytest.mark.parametrize("family", list(FAM))
 def test_no_token_reaches_another_sequence(cuda_ok, family):
     """A sequence of NaN and infinities between two others in the same chunk's rows leaves them bit for bit as without it."""

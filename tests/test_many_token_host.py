@@ -135,3 +135,47 @@ def test_plain_recurrence_is_the_oracles(family):
         o = sess.flush({x: d[x][t:t + 1] for x in ("q", "k", "v", "gate", "beta")})
         np.testing.assert_allclose(out[t], o[0], rtol=1e-12, atol=1e-12)
     np.testing.assert_allclose(S, sess.S, rtol=1e-12, atol=1e-12)
+
+
+def test_calls_go_to_the_layers_device(L, monkeypatch):
+    """prefill, save and restore of a layer whose device is not the current one: that device is current while the
+    call's output is allocated and the kernel launched, on its own current stream or the stream given."""
+    import contextlib
+
+    import torch
+    from ssm_decode_b200 import layer as M
+    now, seen = {"device": 0, "stream": {0: "s0", 1: "s1"}}, []
+
+    @contextlib.contextmanager
+    def on(key, value):
+        was, now[key] = now[key], value
+        yield
+        now[key] = was
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now["device"])
+    monkeypatch.setattr(torch.cuda, "device", lambda d: on("device", torch.device(d).index))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: on("stream", {**now["stream"], now["device"]: s}))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now["stream"][now["device"]])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: "raw " + now["stream"][i], raising=False)
+    monkeypatch.setattr(torch, "zeros", lambda *a, device, **kw: seen.append(("zeros", device.index, now["device"], torch.cuda.current_stream())))
+    monkeypatch.setattr(M.B, "make_prefill_io", lambda *a: None)
+    monkeypatch.setattr(M.B, "_index", lambda *a: None)
+    for f in ("ss_prefill", "ss_cache_write", "ss_cache_read"):
+        monkeypatch.setattr(M.B, f, lambda *a, f=f: seen.append((f, now["device"], a[-1])))
+    lay = M.DecodeLayer.__new__(M.DecodeLayer)
+    lay.plan, lay.heads, lay.dv, lay.batch, lay._bufs = None, 2, 64, 1, {False: None}
+    lay.state = type("State", (), {"device": torch.device("cuda:1")})()
+    cache = type("Cache", (), {"arg": lambda self, layer: None})()
+    q = torch.empty(3, 2, 64)
+    for current in (0, 1):
+        now["device"] = current
+        for given in (None, "mine"):
+            del seen[:]
+            lay.prefill(q, q, q, None, None, None, stream=given)
+            lay.save(cache, None, stream=given)
+            lay.restore(cache, None, stream=given)
+            own = given or "s1"
+            handle = "raw s1" if given is None and current == 1 else own
+            assert seen == [("zeros", 1, 1, own), ("ss_prefill", 1, handle), ("ss_cache_write", 1, handle),
+                            ("ss_cache_read", 1, handle)]
+            assert now["device"] == current and now["stream"] == {0: "s0", 1: "s1"}
