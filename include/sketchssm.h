@@ -353,8 +353,10 @@ ss_status ss_step_mixed(ss_plan* plan, const ss_buffers* bufs, const ss_step_io*
  * no rows in the call; their buffered tokens and fill counts stay valid.
  * State, products and sums are fp32; out is rounded once.  Two forms of the
  * same recurrence exist: token by token with the state in registers, and
- * (Mamba-2, GDN) chunks of 64 tokens on the tensor cores, which runs from
- * max_tokens = 32 on (48 with dk or dv = 64, 64 with both); bf16 operands are
+ * (Mamba-2, GDN) chunks of 64 tokens on the tensor cores, which runs where it
+ * is the faster one for max_tokens: from 20 tokens on (24 with dk = dv = 64)
+ * while batch * heads is at most the number of SMs, from 32 on at dk = dv = 128
+ * (44 at 64 x 128, 57 at 128 x 64, 110 at 64 x 64) for thousands.  Operands are
  * cut so that its products are fp32 ones up to 2^-21.  Inputs are expected to
  * be finite: a NaN or infinity in a token reaches the state and the later
  * outputs, and in the chunked form it may reach the outputs of the (at most

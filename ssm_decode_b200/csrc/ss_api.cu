@@ -40,14 +40,6 @@ namespace {
 thread_local std::string g_err;
 std::atomic<uint64_t> g_launches{0};
 constexpr int kSmemLimit = 227 * 1024;
-// ss_prefill runs the chunked form from this longest sequence on.  A chunk of
-// 64 tokens costs about the same however few tokens are in it, a token of the
-// other form dk dv multiply-adds.  Measured, tokens / chunks in us: 128 x 128
-// GDN, 256 x 32 heads, 24 tokens 657 / 870, 32 tokens 838 / 871, 48 tokens 1248 /
-// 881; one sequence x 32 heads, 24 tokens 18 / 16; 128 x 64 Mamba-2, 64 x 128
-// heads, 32 tokens 360 / 533, 48 tokens 529 / 541; 64 x 64 GDN, 64 x 8 heads, 64
-// tokens 51 / 49.
-int64_t chunk_tokens(const ss_config& c) { return 32 + (c.dk == 64 ? 16 : 0) + (c.dv == 64 ? 16 : 0); }
 
 ss_status fail(ss_status s, const char* fmt, ...) {
     char buf[512];
@@ -618,7 +610,7 @@ ss_status ss_prefill(ss_plan* pl, const ss_buffers* b, const ss_prefill_io* io, 
     p.B = c.batch; p.H = c.heads; p.group = c.heads / qh;
     p.out_bf16 = io->out_dtype == SS_BF16;
     const int64_t longest = io->max_tokens == 0 ? io->rows : io->max_tokens;
-    const bool chunks = !kda && io->rows > 0 && longest >= chunk_tokens(c);
+    const bool chunks = !kda && io->rows > 0 && ss::prefill_chunks_pay(c.dk, c.dv, int64_t(c.batch) * c.heads, longest);
     p.stall = chunks ? take_stall(pl) : 0;       // (the token form has no bulk copies: the hook stays armed)
     // (sequences of much the same length too: two rounds of them then end together)
     p.order = c.batch > 1 && c.batch <= ss::PREFILL_ORDER_MAX;

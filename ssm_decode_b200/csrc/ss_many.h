@@ -43,6 +43,8 @@ struct CacheParams {
 cudaError_t launch_prefill_tokens(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream);
 // The same in chunks of 64 tokens on the tensor cores (Mamba-2, GDN).
 cudaError_t launch_prefill_chunks(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream);
+// Whether that is the faster one for `units` = batch * heads and a longest sequence of `longest` tokens.
+bool prefill_chunks_pay(int dk, int dv, long long units, long long longest);
 // States into / out of quantised slots.
 cudaError_t launch_cache_write(int bits, const CacheParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(int bits, const CacheParams& p, cudaStream_t stream);

@@ -691,6 +691,27 @@ cudaError_t chunks_dispatch(int dk, int dv, const PrefillParams& p, cudaStream_t
 
 }  // namespace
 
+// The chunked form's time goes by the chunks of 64 tokens, full or not, and by
+// the waves of units over the SMs, one a CTA; the token form's by the tokens: a
+// latency of half a microsecond each while its CTAs have SMs to themselves, dk dv
+// multiply-adds each once they do not.  So the first chunk pays from a number of
+// tokens that grows with the waves and with how small the state is, a later one
+// from 3 / 8 of it more.  Measured on equal lengths, tokens / chunks in us:
+//   one wave   GDN 1 x 32 heads, 128 x 128: 20 tokens 14.4 / 15.9, 24 16.4 / 15.7, 64 34 / 15.5;
+//              64 x 64, 4 x 32 heads: 24 tokens 14.8 / 15.4, 28 15.9 / 15.2
+//   to four    GDN 16 x 32 heads: 128 x 128, 24 tokens 50 / 54, 28 57 / 54; 64 x 128, 32 44 / 50, 40 53 / 51;
+//              128 x 64, 40 48 / 53, 48 56 / 53; 64 x 64, 48 47 / 48.  8 x 32 heads, 128 x 64: 32 26 / 29, 40 31 / 29
+//   more       GDN 256 x 32 heads: 128 x 128, 32 tokens 843 / 879, 40 1057 / 879; 64 x 128, 48 758 / 823, 56 884 / 824;
+//              128 x 64, 56 739 / 847, 80 1035 / 1155, 96 1238 / 1159; 64 x 64, 112 884 / 1077, 160 1257 / 1364.
+//              Mamba-2 64 x 32 heads: 128 x 128, 28 167 / 162; 64 x 128, 40 147 / 135; 128 x 64, 56 164 / 147,
+//              65 189 / 196; 64 x 64, 64 119 / 125, 96 175 / 168, 112 203 / 169
+bool prefill_chunks_pay(int dk, int dv, long long units, long long longest) {
+    static constexpr int from[2][2][3] = {{{24, 44, 80}, {20, 30, 44}}, {{20, 38, 57}, {20, 24, 32}}};
+    longest = longest < 0x7fffffffLL ? longest : 0x7fffffffLL;          // (a bound: any number may be given)
+    const long long waves = (units + sm_count() - 1) / sm_count(), chunks = (longest + C - 1) / C;
+    return longest * 8 >= from[dk == 128][dv == 128][waves <= 1 ? 0 : waves <= 4 ? 1 : 2] * (5 + 3 * chunks);
+}
+
 cudaError_t launch_prefill_chunks(int family, int dk, int dv, const PrefillParams& p, cudaStream_t stream) {
     if (family == GDN) return chunks_dispatch<GDN>(dk, dv, p, stream);
     if (family == MAMBA2) return chunks_dispatch<MAMBA2>(dk, dv, p, stream);

@@ -76,3 +76,21 @@ def test_a_prompt_in_parts_of_whole_chunks_is_the_same_bits(cuda_ok, family):
         torch.cuda.synchronize()
         got.append((out.cpu(), lay.state.cpu()))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("dk,dv,batch,heads,tokens,chunks", [
+    (128, 128, 1, 2, 24, True), (128, 128, 1, 2, 16, False), (128, 128, 64, 32, 28, False), (128, 128, 64, 32, 40, True),
+    (64, 64, 1, 2, 32, True), (64, 64, 64, 32, 64, False), (128, 64, 64, 32, 52, False), (128, 64, 64, 32, 70, False),
+    (64, 128, 16, 32, 40, True)])
+def test_the_faster_form_runs(cuda_ok, dk, dv, batch, heads, tokens, chunks):
+    """Which form a call takes, by the shape, the number of units and the longest sequence: the testing hook that
+    delays a bulk copy reaches the chunked form only.  (Measured both ways at each of these; the two differ by 5 to 50 %.)"""
+    import torch
+    from ssm_decode_b200 import binding as B
+    d = U.draw(synth.GDN, tokens, heads, 1, dk, dv, 33)
+    lay = DecodeLayer(synth.GDN, batch, heads, dk, dv, 4, [2] * heads)
+    st = starts([tokens] + [0] * (batch - 1))
+    B.ss_debug_stall_next_copy(lay.plan)
+    lay.prefill(*(dev(d[x]) for x in ("q", "k", "v", "gate", "beta")), st, max_tokens=tokens)
+    torch.cuda.synchronize()
+    assert int(lay.status[0]) == (B.SS_DEVICE_TIMEOUT if chunks else 0)
