@@ -64,14 +64,15 @@ __global__ void __launch_bounds__(2 * VC, K == 128 ? 4 : 6) prefill_tokens_kerne
     const int col0 = int(blockIdx.x % splits) * VC;
     const int b = int(u / p.H), h = int(u % p.H);
     griddep_wait();
-    griddep_launch_next();
     int first, count;
-    if (!seq_rows(p, b, first, count)) {
-        if (t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
-        return;
-    }
+    if (!seq_rows<true>(p, b, first, count)) return;
     const bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
     if (count == 0 && !fresh) return;
+    // The next launch starts early over a few tokens.  Over a prompt its CTAs would
+    // settle unevenly on the SMs that fall idle first and keep those places: KDA
+    // prompts of 300 to 512 tokens, calls back to back, 508 us with it, 457
+    // without; 4 tokens 208 and 212.
+    if (count <= TOK) griddep_launch_next();
 
     const int rg = lane >> 2, cg = lane & 3;
     const int wc = warp * 16 + cg * 4;                    // the lane's first column within the CTA

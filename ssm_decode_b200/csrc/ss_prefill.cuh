@@ -6,10 +6,14 @@
 
 namespace ss {
 
-// The row range of sequence b; false if it is not a range of the call's rows.
+// The row range of sequence b; false (with REPORT and the status bit) if it is not a range of the call's rows.
+template <bool REPORT>
 __device__ __forceinline__ bool seq_rows(const PrefillParams& p, int b, int& first, int& count) {
     const int s = p.seq_start[b], e = p.seq_start[b + 1];
-    if (s < 0 || e < s || e > p.rows) return false;
+    if (s < 0 || e < s || e > p.rows) {
+        if (REPORT && threadIdx.x == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
+        return false;
+    }
     first = s;
     count = e - s;
     return true;

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     // with another kernel between); equal lengths lose nothing (237 and 237 us).
     const int h = int(blockIdx.x % unsigned(p.H));
     int b = int(blockIdx.x / unsigned(p.H)), first, count;
-    const bool good = seq_rows(p, b, first, count);
+    const bool good = seq_rows<false>(p, b, first, count);
     if (!good && t == 0 && p.status != nullptr) atomicOr(p.status, SS_DEVICE_BAD_ROWS);
     bool fresh = p.fresh != nullptr && p.fresh[b] != 0;
     if (good && count == 0 && fresh) {                         // no token: the state only starts afresh
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(NT, 1) prefill_chunks_kernel(const __grid_cons
     }
     if (p.order) {
         b = sequence_at<NT>(p, b, reinterpret_cast<int*>(sm + L.a));     // (no copy lands in this scratch)
-        if (b < 0 || !seq_rows(p, b, first, count)) return;
+        if (b < 0 || !seq_rows<false>(p, b, first, count)) return;
         fresh = p.fresh != nullptr && p.fresh[b] != 0;
     } else if (!good) {
         return;

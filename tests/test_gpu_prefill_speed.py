@@ -10,15 +10,17 @@ from tests.test_gpu_prefill import dev, starts
 pytestmark = pytest.mark.gpu
 
 
-def test_ragged_calls_back_to_back(cuda_ok):
+@pytest.mark.parametrize("family,lens", [
+    (synth.GDN, [4096, 3689, 1867, 1477, 1458, 1202, 934, 868, 232, 44, 35, 16, 4, 2, 1, 1]),
+    (synth.KDA, [512, 300, 447, 342, 402, 497, 339, 377])])
+def test_ragged_calls_back_to_back(cuda_ok, family, lens):
     """Calls of a ragged batch, one right behind the other, take no longer than with another kernel between them:
     the next call's blocks do not settle among the last ones of the call before.  (Before they were kept out the
-    first way took 1.18 times the second; without, 0.99.)"""
+    first way took 1.18 (GDN) and 1.08 (KDA) times the second; without, 0.99.)"""
     import torch
-    lens = [4096, 3689, 1867, 1477, 1458, 1202, 934, 868, 232, 44, 35, 16, 4, 2, 1, 1]
     H, D = 32, 128
-    d = U.draw(synth.GDN, sum(lens), H, 1, D, D, 30)
-    lay = DecodeLayer(synth.GDN, len(lens), H, D, D, 4, [2] * H)
+    d = U.draw(family, sum(lens), H, 1, D, D, 30)
+    lay = DecodeLayer(family, len(lens), H, D, D, 4, [2] * H)
     args = [dev(d[x]) for x in ("q", "k", "v", "gate", "beta")] + [starts(lens)]
     out = torch.zeros(sum(lens), H, D, device="cuda")
     small = torch.zeros(32, device="cuda")
@@ -36,4 +38,4 @@ def test_ragged_calls_back_to_back(cuda_ok):
 
     time(False), time(True)
     t = np.array([[time(False), time(True)] for _ in range(8)]).min(0)
-    assert t[0] <= 1.08 * t[1], f"{t[0] * 1e3:.0f} us back to back, {t[1] * 1e3:.0f} us with a kernel between"
+    assert t[0] <= 1.04 * t[1], f"{t[0] * 1e3:.0f} us back to back, {t[1] * 1e3:.0f} us with a kernel between"
