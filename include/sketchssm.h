@@ -202,7 +202,8 @@ typedef struct {
                              /* elements; q, k, v, out multiples of 8, KDA's gate of 4; at least a dense row */
     int64_t rows;            /* token rows of the tensors, 0 .. 2^31 - 1 (0: the six pointers are not read) */
     int64_t max_tokens;      /* at least the longest sequence's tokens, or 0 = rows; picks the form that
-                              * runs (see ss_prefill), never what is computed */
+                              * runs (see ss_prefill): the two compute the same and differ in rounding,
+                              * and in what a token that is not finite reaches */
     const int32_t* seq_start;/* device int32[batch+1], 4-byte aligned */
     const int32_t* fresh;    /* device int32[batch], 4-byte aligned, or NULL; nonzero: the sequence starts
                               * from a zero state, and bufs->state is only written for it */
@@ -347,18 +348,26 @@ ss_status ss_step_mixed(ss_plan* plan, const ss_buffers* bufs, const ss_step_io*
  * A sequence of no tokens keeps its state (a fresh one becomes zero); output
  * rows of no sequence are left as they were.  Sequences whose rows overlap
  * each other race for the output rows they share; nothing else does.
+ * The state is updated in place and keeps no earlier one: to be able to take
+ * only the first tokens of a draft, copy the states before the call (a cache
+ * slot holds them rounded) and run the accepted tokens on the copy.
  * Legal at phase 0 (nothing buffered); needs bufs->state (and A for Mamba-2).
- * Marks the sketch stale: ss_prime comes before the next non-flush step.  In
- * a batch driven by ss_step_mixed, sequences that have tokens buffered take
- * no rows in the call; their buffered tokens and fill counts stay valid.
+ * Marks the sketch stale: ss_prime, which reads every sequence's state, comes
+ * before the next non-flush step, whichever sequences had tokens.  In a batch
+ * driven by ss_step_mixed, sequences that have tokens buffered take no rows in
+ * the call; their buffered tokens and fill counts stay valid.
  * State, products and sums are fp32; out is rounded once.  Two forms of the
  * same recurrence exist: token by token with the state in registers, and
  * (Mamba-2, GDN) chunks of 64 tokens on the tensor cores, which runs where it
  * is the faster one for max_tokens: from 20 tokens on (24 with dk = dv = 64)
  * while batch * heads is at most the number of SMs, from 32 on at dk = dv = 128
  * (44 at 64 x 128, 57 at 128 x 64, 110 at 64 x 64) for thousands.  Operands are
- * cut so that its products are fp32 ones up to 2^-21.  Inputs are expected to
- * be finite: a NaN or infinity in a token reaches the state and the later
+ * cut so that its products are fp32 ones up to 2^-21.  A call runs in one form:
+ * one prompt among drafts makes a whole chunk of each of them, so prompts and
+ * drafts are faster in calls of their own (in each, the others' sequences have
+ * no rows and are not fresh).  Decays are expected to be at most 1: the chunked form needs the
+ * products of a chunk's 64 to be fp32 numbers.  Inputs are expected to be
+ * finite: a NaN or infinity in a token reaches the state and the later
  * outputs, and in the chunked form it may reach the outputs of the (at most
  * 63) tokens before it in its chunk, never another sequence. */
 ss_status ss_prefill(ss_plan* plan, const ss_buffers* bufs, const ss_prefill_io* io, ss_stream stream);

@@ -19,11 +19,14 @@
 // number of values each time, and u comes back by 4.  A CTA is 64 columns of a
 // head, four warps: whole heads (eight warps) left the loads, the tokens and the
 // stores of fewer CTAs to overlap (GDN, 256 x 32 heads, 4 tokens: 248 us against
-// 207), two warps staged k and q too often (KDA prompts 485 against 453 us).
+// 203), two warps staged k and q too often (KDA prompts 485 against 453 us).
 //
 // What bounds it: for a few tokens the state, read and written once (128 KB a
 // head at 128 x 128); beyond about ten tokens the fp32 pipe and its issue
-// slots, 3 dk dv multiply-adds a token and KDA's dk dv decays.
+// slots: a state value takes one multiply (its decay) and three multiply-adds a
+// token, Mamba-2's two.  256 x 32 heads, 128 x 128, bf16 out, calls back to back,
+// in us by tokens: GDN 1 165, 4 195, 8 269, 16 455, 24 661, 31 819; KDA 172, 205,
+// 289, 480, 690, 858 (floors 165 and 166 for one token, 195 and 210 for 24).
 #include "ss_prefill.cuh"
 
 namespace ss {

@@ -23,8 +23,8 @@ __device__ __forceinline__ bool seq_rows(const PrefillParams& p, int b, int& fir
 // (every thread of the block calls it; scratch: PREFILL_ORDER_MAX + 1 ints).  Blocks
 // start in order, so the long sequences do not begin last, the blocks that have
 // work are dealt out over the SMs, and those that have none end at once: one
-// prompt of 512 tokens in a batch of 256 x 32 heads takes 74 us, not 225 (alone
-// 54).  The token form does without: its blocks end at once by themselves, and
+// prompt of 512 tokens in a batch of 256 x 32 heads takes 70 us, not 225 (alone
+// 53).  The token form does without: its blocks end at once by themselves, and
 // the registers that this costs it made every call about a tenth slower.
 template <int THREADS>
 __device__ __forceinline__ int sequence_at(const PrefillParams& p, int place, int* scratch) {

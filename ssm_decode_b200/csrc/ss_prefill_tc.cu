@@ -51,9 +51,11 @@
 // D1 2.2 k, R 1.1 k, X 2.1 k, t o U 1.2 k, update and sum 1.4 k) and the staging
 // warps' (decays 1.7 k, the solve 5.5 k, parts 1.8 k).  Each warp runs its
 // straight-line code at about four cycles an instruction, instruction fetches
-// being the largest stall after the waits; the tensor pipe is active 30 % of the
-// time (60 MMAs of 77 cycles, whatever N up to 128, and the Gram products).
-// 8192 tokens x 32 heads take 700 us (32 of 148 SMs), 16 x 1024 tokens 438 us.
+// being the largest stall after the waits; the tensor pipe works for 4.6 k of the
+// 10.2 k (60 MMAs of 77 cycles, whatever N up to 128) and the 8 Gram MMAs; 30 % is
+// its share of a whole cold launch of 16 chunks, with its start and state loads.
+// 8192 tokens x 32 heads take 703 us (32 of 148 SMs), 16 x 1024 tokens 422 to 446 us
+// by the GPU.
 // Measured and left out: the inverse by 16 x 16 blocks (fp32 tiles 400 against
 // 350 us for 4096 tokens x 32 heads; warp-level tf32 or bf16 MMAs wait for the
 // tcgen05 ones, 400 cycles and more a block), 8 staging or 16 worker warps

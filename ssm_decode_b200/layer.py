@@ -151,10 +151,13 @@ class DecodeLayer:
         (device int32 [batch + 1]).  Rows may be strided, and qk_heads may
         divide heads (shared keys).  max_tokens (a host int, at least the
         longest sequence) lets the library pick the faster form; None takes
-        the number of rows, so give it for short drafts of many sequences.  Returns out [rows][heads][dv], allocated in
-        `out_dtype` (bf16 unless given) when not passed; rows of no sequence
-        are left as they were (zero in an allocated one).  Needs phase 0;
-        prime() comes before the next sketched step."""
+        the number of rows, so give it for short drafts of many sequences, and
+        give prompts and drafts in calls of their own.  Returns out
+        [rows][heads][dv], allocated in `out_dtype` (bf16 unless given) when
+        not passed; rows of no sequence are left as they were (zero in an
+        allocated one).  The state is updated in place: clone it first to be
+        able to reject part of a draft.  Needs phase 0; prime(), over the
+        whole batch, comes before the next sketched step."""
         import torch
         with self._on_device(stream) as st:
             if out is None:
